@@ -74,12 +74,16 @@ typedef enum {
  * scale per weight row (moe_quantize_rows_e4m3); only moe_forward_fp8 takes it.
  * MOE_DTYPE_MXFP8: bf16 activations with MXFP8 expert weights, E4M3 codes with
  * one E8M0 scale per block of 32 (moe_quantize_mx); only moe_forward_mx takes
- * it. */
+ * it.
+ * MOE_DTYPE_MXFP4: bf16 activations with MXFP4 expert weights, E2M1 codes with
+ * one E8M0 scale per block of 32 (moe_quantize_mxfp4); only moe_forward_mxfp4
+ * takes it. */
 typedef enum {
   MOE_DTYPE_F32 = 0,
   MOE_DTYPE_BF16 = 1,
   MOE_DTYPE_E4M3 = 2,
-  MOE_DTYPE_MXFP8 = 3
+  MOE_DTYPE_MXFP8 = 3,
+  MOE_DTYPE_MXFP4 = 4
 } moe_dtype;
 
 /* Token-tile choice of the grouped GEMMs. AUTO: a batch of T <= 64 tokens
@@ -268,8 +272,10 @@ moe_status moe_down_combine_noalloc(const moe_problem* pb, const void* h, const 
  * slot_pos, h, h_shared. Each is -1 when absent. MXFP8 problems that run the
  * decode-sized kernels (moe_forward_mx) store h and h_shared as E4M3 codes
  * with E8M0 scale rows (moe_mx_scale_cols(I) and (I_shared) bytes per row) at
- * h_scales and h_shared_scales; otherwise those two are -1 and h holds the
- * layer's activation values (bf16 or fp32). */
+ * h_scales and h_shared_scales; MXFP4 problems store E4M3 codes too, with
+ * their scales in the token-tile form of the MXFP4 products (internal) there.
+ * Otherwise those two are -1 and h holds the layer's activation values (bf16
+ * or fp32). */
 typedef struct {
   int64_t logits, topk_ids, topk_w, expert_offsets, gather_idx, slot_pos, h, h_shared;
   int64_t h_scales, h_shared_scales;
@@ -347,6 +353,77 @@ moe_status moe_forward_mx(const moe_problem* pb, const void* x, const void* W_ro
                           const uint8_t* Wsq_up, const uint8_t* ss_up, const uint8_t* Wsq_down,
                           const uint8_t* ss_down, void* y, void* workspace,
                           size_t workspace_bytes, void* stream);
+
+/* MXFP4: E2M1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives) with one
+ * E8M0 scale per 32 consecutive elements of a row (the last block of a row may
+ * hold fewer). Per block, with amax its largest magnitude:
+ *   e = max(floor(log2(amax)) - 2, -127); e = -127 for zeros;
+ *   scale byte = e + 127; codes = E2M1(v / 2^e), nearest even, saturating at 6;
+ *   a block that holds an infinity or a NaN has the scale byte 255 (NaN): all
+ *   of its elements read back as NaN.
+ * A matrix [rows][cols] is stored as
+ *   codes: moe_mxfp4_code_cols(cols) = 64 ceil(cols / 128) bytes per row, two
+ *     codes to a byte, the even element in the low half; zeros past the row;
+ *   scales: moe_mxfp4_scale_bytes(rows, cols) bytes, tiles of 128 rows x 4
+ *     blocks of 512 bytes each, row r and block b of a tile at byte
+ *     16 (r % 32) + 4 (r / 32) + b; the tiles are row-major over
+ *     ceil(rows / 128) x ceil(cols / 128); zeros outside the matrix.
+ * src [rows][cols] bf16 or fp32 (src_dtype) with a row stride of ld elements
+ * (ld >= cols; any alignment of the element type; rows of 16-byte aligned
+ * starts are read faster) -> q, scales (16-byte aligned). */
+int64_t moe_mxfp4_code_cols(int64_t cols);
+int64_t moe_mxfp4_scale_bytes(int64_t rows, int64_t cols);
+moe_status moe_quantize_mxfp4(const void* src, int32_t src_dtype, int64_t rows, int64_t cols,
+                              int64_t ld, uint8_t* q, uint8_t* scales, void* stream);
+
+/* The gate and up matrices [E][I][H] (bf16 or fp32, 16-byte aligned) of an
+ * expert layer as one MXFP4 matrix of E * 2I rows, in which gate and up rows
+ * alternate in runs of 64: row e 2I + 128 (f / 64) + f % 64 is gate feature f of
+ * expert e, and the up feature lies 64 rows further. I a multiple of 64. */
+moe_status moe_quantize_mxfp4_gate_up(const void* W_gate, const void* W_up, int32_t src_dtype,
+                                      int64_t E, int64_t I, int64_t H, uint8_t* q, uint8_t* scales,
+                                      void* stream);
+
+/* The values an MXFP4 matrix stands for: out [rows][cols] bf16 or fp32
+ * (out_dtype) with a row stride of ld elements. Exact in both types. */
+moe_status moe_dequantize_mxfp4(const uint8_t* q, const uint8_t* scales, int64_t rows, int64_t cols,
+                                void* out, int32_t out_dtype, int64_t ld, void* stream);
+
+/* Dense product with MXFP4 weights: y[t][n] = sum_k xq[t][k] W[n][k] for x
+ * [T][K] (bf16, row stride ld_x) and W [N][K] (Wq, s_W: moe_quantize_mxfp4 of
+ * the N rows; Wq 32-byte aligned). x is quantized on entry per 32 elements of a
+ * row: act_dtype MOE_DTYPE_MXFP8 (E4M3 codes, e = max(floor(log2(amax)) - 8,
+ * -127), saturating at 448) or MOE_DTYPE_MXFP4 (as above); a block of x that
+ * holds an infinity or a NaN makes its token's row of y NaN. fp32
+ * accumulation, one rounding to y_dtype (bf16 or fp32); y has the row stride
+ * ld_y. Any T >= 0, N >= 1, K >= 1; x and y need the alignment of their
+ * elements only. The workspace (moe_linear_mxfp4_workspace_size bytes) holds
+ * the status word, the quantized x and partial sums. */
+moe_status moe_linear_mxfp4_workspace_size(int64_t T, int64_t N, int64_t K, int32_t act_dtype,
+                                           size_t* bytes);
+moe_status moe_linear_mxfp4(const void* x, int64_t T, int64_t K, int64_t ld_x, int32_t act_dtype,
+                            const uint8_t* Wq, const uint8_t* s_W, int64_t N, void* y,
+                            int32_t y_dtype, int64_t ld_y, void* workspace, size_t workspace_bytes,
+                            void* stream);
+
+/* The layer with MXFP4 expert weights: pb->dtype = MOE_DTYPE_MXFP4; x,
+ * W_router and y are bf16 (y fp32 with out_f32); routing and permutation as
+ * moe_forward (on x itself). Weights: Wq_gate_up, s_gate_up from
+ * moe_quantize_mxfp4_gate_up; Wq_down, s_down from moe_quantize_mxfp4 of W_down
+ * viewed as [E*H][I]; the shared expert's likewise ([I_s] rows each of gate and
+ * up; [H][I_s]; all NULL iff I_shared == 0). Codes are 32-byte, scales 16-byte
+ * aligned. Per forward pass the token rows are quantized to MXFP8 in blocks of
+ * 32 along H, and h = silu(g) * u from fp32 in blocks of 32 along I (rules as
+ * in moe_linear_mxfp4); both GEMMs multiply the codes and apply the scales in
+ * the tensor cores, with fp32 accumulation; the combine is moe_forward's.
+ * Requires I and I_shared multiples of 128. Workspace: moe_workspace_size(pb). */
+moe_status moe_forward_mxfp4(const moe_problem* pb, const void* x, const void* W_router,
+                             const float* router_bias, const uint8_t* Wq_gate_up,
+                             const uint8_t* s_gate_up, const uint8_t* Wq_down,
+                             const uint8_t* s_down, const uint8_t* Wsq_gate_up,
+                             const uint8_t* ss_gate_up, const uint8_t* Wsq_down,
+                             const uint8_t* ss_down, void* y, void* workspace,
+                             size_t workspace_bytes, void* stream);
 
 /* Synchronises `stream`, then copies the device status word into *out. */
 moe_status moe_get_device_status(const void* workspace, void* stream, moe_status* out);

@@ -5,18 +5,22 @@ include/moe_api.h); this package only marshals torch tensors into it:
 
 * ``_binding``: one Python function per C entry point, same names.
 * ``MoELayer``: holds the expert weights on the GPU and a workspace, and runs
-  ``moe_forward`` on the current torch stream.
+  ``moe_forward`` on the current torch stream. ``MoELayerFP8``, ``MoELayerMX``
+  and ``MoELayerMXFP4``: the same with quantized expert weights.
+* ``LinearMXFP4``: a dense product with MXFP4 weights.
 """
 from __future__ import annotations
 
 import torch
 
 from ._binding import (  # noqa: F401
-    EXPORTED, MOE_DTYPE_BF16, MOE_DTYPE_E4M3, MOE_DTYPE_F32, MOE_DTYPE_MXFP8,
+    EXPORTED, MOE_DTYPE_BF16, MOE_DTYPE_E4M3, MOE_DTYPE_F32, MOE_DTYPE_MXFP4, MOE_DTYPE_MXFP8,
     MOE_FLAG_TEST_SKIP_SIGNAL, MOE_OK, MOE_TILE_AUTO, MOE_TILE_DECODE, MOE_TILE_MEDIUM,
-    MOE_TILE_PREFILL, STATUS_NAMES, MoEError, MoEProblem, down_combine, down_combine_noalloc,
-    forward, forward_fp8, forward_mx, forward_single_launch, get_device_status,
-    grouped_swiglu_gemm, load_library, make_problem, mx_scale_cols, permute, quantize_mx,
+    MOE_TILE_PREFILL, STATUS_NAMES, MoEError, MoEProblem, _check_mxfp4, dequantize_mxfp4,
+    down_combine, down_combine_noalloc, forward, forward_fp8, forward_mx, forward_mxfp4,
+    forward_single_launch, get_device_status, grouped_swiglu_gemm, linear_mxfp4,
+    linear_mxfp4_workspace_size, load_library, make_problem, mx_scale_cols, mxfp4_code_cols,
+    mxfp4_scale_bytes, permute, quantize_mx, quantize_mxfp4, quantize_mxfp4_gate_up,
     quantize_rows_e4m3, reset_device_status, route, route_grouped, router_logits, status_string,
     workspace_layout, workspace_size)
 
@@ -164,3 +168,143 @@ class MoELayerMX(_QuantizedLayer):
     _dtype_name = "mxfp8"
     _quantize = staticmethod(quantize_mx_rows)
     _forward = staticmethod(forward_mx)
+
+
+def quantize_mxfp4_rows(W: torch.Tensor, stream=None):
+    """(codes uint8 [..., mxfp4_code_cols(cols)], tiled scales uint8) of W viewed
+    as rows of its last dimension, by moe_quantize_mxfp4 (E2M1 with one
+    power-of-two scale per block of 32 elements). A matrix may have any row
+    stride; W of more dimensions is contiguous."""
+    cols = W.shape[-1]
+    rows = W.numel() // cols
+    q = torch.empty(W.shape[:-1] + (mxfp4_code_cols(cols),), dtype=torch.uint8, device=W.device)
+    s = torch.empty(mxfp4_scale_bytes(rows, cols), dtype=torch.uint8, device=W.device)
+    quantize_mxfp4(W if W.dim() == 2 else W.view(rows, cols), q, s, stream)
+    return q, s
+
+
+def dequantize_mxfp4_rows(q: torch.Tensor, s: torch.Tensor, rows: int, cols: int,
+                          dtype=torch.bfloat16, stream=None):
+    """The values [rows, cols] (bf16 or fp32) of an MXFP4 matrix."""
+    out = torch.empty(rows, cols, dtype=dtype, device=q.device)
+    dequantize_mxfp4(q, s, out, stream)
+    return out
+
+
+class LinearMXFP4:
+    """y = x W^T on one GPU with MXFP4 weights W [N, K], quantized once from a
+    bf16 or fp32 matrix. x [T, K] is bf16 and quantized on entry, to MXFP8
+    (act="mxfp8") or MXFP4 (act="mxfp4")."""
+
+    def __init__(self, W: torch.Tensor, act: str = "mxfp8"):
+        q, s = quantize_mxfp4_rows(W)
+        self._set(q, s, W.shape[0], W.shape[1], act)
+
+    @classmethod
+    def from_quantized(cls, q, s, N: int, K: int, act: str = "mxfp8"):
+        """From codes and scales in the layout of moe_quantize_mxfp4."""
+        self = cls.__new__(cls)
+        self._set(q, s, N, K, act)
+        return self
+
+    def _set(self, q, s, N, K, act):
+        if act not in ("mxfp8", "mxfp4"):
+            raise ValueError(f"act: 'mxfp8' or 'mxfp4' expected, got {act!r}")
+        _check_mxfp4(q, s, N, K, "W")
+        self.q, self.s, self.N, self.K = q, s, N, K
+        self.act = MOE_DTYPE_MXFP8 if act == "mxfp8" else MOE_DTYPE_MXFP4
+        self._ws = {}
+
+    def workspace(self, T: int) -> torch.Tensor:
+        ws = self._ws.get(T)
+        if ws is None:
+            n = linear_mxfp4_workspace_size(T, self.N, self.K, self.act)
+            ws = torch.zeros(n, dtype=torch.uint8, device=self.q.device)
+            self._ws[T] = ws
+        return ws
+
+    def forward(self, x, out=None, stream=None, out_f32=False):
+        """y [T, N], bf16 or (out_f32) fp32, for x [T, K] of any row stride."""
+        if x.dim() != 2 or x.shape[1] != self.K:
+            raise ValueError(f"x: [T, {self.K}] expected, got {tuple(x.shape)}")
+        T = x.shape[0]
+        odt = torch.float32 if out_f32 else torch.bfloat16
+        y = out if out is not None else torch.empty((T, self.N), dtype=odt, device=x.device)
+        linear_mxfp4(x, self.act, self.q, self.s, self.N, y, self.workspace(T), stream)
+        return y
+
+    __call__ = forward
+
+
+class MoELayerMXFP4(_QuantizedLayer):
+    """The layer with MXFP4 expert weights and MXFP8 activations
+    (moe_forward_mxfp4), quantized once on the GPU from the same weights
+    MoELayer takes, or given in the quantized layout (from_quantized)."""
+
+    _dtype_name = "mxfp4"
+
+    def __init__(self, W_router, W_gate, W_up, W_down, k, router_bias=None, Ws_gate=None,
+                 Ws_up=None, Ws_down=None, renorm=1, tile=MOE_TILE_AUTO, n_group=1,
+                 topk_group=1):
+        E, I, H = W_gate.shape
+        shared = Ws_gate is not None
+        self._set(W_router, self._gate_up(W_gate, W_up), quantize_mxfp4_rows(W_down), k,
+                  router_bias,
+                  self._gate_up(Ws_gate[None], Ws_up[None]) if shared else (None, None),
+                  quantize_mxfp4_rows(Ws_down) if shared else (None, None), renorm, tile,
+                  n_group, topk_group, (E, I, H), Ws_gate.shape[0] if shared else 0)
+
+    @staticmethod
+    def _gate_up(W_gate, W_up):
+        E, I, H = W_gate.shape
+        q = torch.empty(E, 2 * I, mxfp4_code_cols(H), dtype=torch.uint8, device=W_gate.device)
+        s = torch.empty(mxfp4_scale_bytes(2 * E * I, H), dtype=torch.uint8, device=W_gate.device)
+        quantize_mxfp4_gate_up(W_gate, W_up, q, s)
+        return q, s
+
+    @classmethod
+    def from_quantized(cls, W_router, gate_up, down, k, router_bias=None, shared_gate_up=None,
+                       shared_down=None, renorm=1, tile=MOE_TILE_AUTO, n_group=1, topk_group=1):
+        """From (codes, scales) pairs: gate_up codes [E, 2I, mxfp4_code_cols(H)]
+        (gate and up rows alternating in runs of 64), down codes
+        [E, H, mxfp4_code_cols(I)], the shared expert's alike without E; scales
+        in tiles (moe_quantize_mxfp4)."""
+        self = cls.__new__(cls)
+        E, I2, _ = gate_up[0].shape
+        Is = shared_gate_up[0].numel() // mxfp4_code_cols(W_router.shape[1]) // 2 \
+            if shared_gate_up is not None else 0
+        self._set(W_router, gate_up, down, k, router_bias, shared_gate_up or (None, None),
+                  shared_down or (None, None), renorm, tile, n_group, topk_group,
+                  (E, I2 // 2, W_router.shape[1]), Is)
+        return self
+
+    def _set(self, W_router, gate_up, down, k, router_bias, shared_gate_up, shared_down, renorm,
+             tile, n_group, topk_group, shape, I_shared):
+        self.W_router, self.router_bias = W_router, router_bias
+        self.E, self.I, self.H = E, I, H = shape
+        self.I_shared = I_shared
+        self.k, self.renorm, self.tile = k, renorm, tile
+        self.n_group, self.topk_group = n_group, topk_group
+        self.dtype = torch.bfloat16  # activations (x, y)
+        _check_mxfp4(*gate_up, 2 * E * I, H, "gate_up")
+        _check_mxfp4(*down, E * H, I, "down")
+        if I_shared:
+            _check_mxfp4(*shared_gate_up, 2 * I_shared, H, "shared_gate_up")
+            _check_mxfp4(*shared_down, H, I_shared, "shared_down")
+        self.gate_up, self.down = gate_up, down
+        self.s_gate_up, self.s_down = shared_gate_up, shared_down
+        self._ws = {}
+
+    def forward(self, x, out=None, stream=None, out_f32=False):
+        if x.dim() != 2 or x.shape[1] != self.H or x.dtype != self.dtype or not x.is_contiguous():
+            raise ValueError(f"x: contiguous bf16 [T, {self.H}] expected, got {x.dtype} "
+                             f"{tuple(x.shape)}")
+        T = x.shape[0]
+        odt = torch.float32 if out_f32 else torch.bfloat16
+        y = out if out is not None else torch.empty((T, self.H), dtype=odt, device=x.device)
+        forward_mxfp4(self.problem(T, out_f32=out_f32), x, self.W_router, self.router_bias,
+                      *self.gate_up, *self.down, *self.s_gate_up, *self.s_down, y,
+                      self.workspace(T), stream)
+        return y
+
+    __call__ = forward

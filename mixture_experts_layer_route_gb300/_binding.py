@@ -18,7 +18,7 @@ MOE_OK = 0
 STATUS_NAMES = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED",
                 3: "MOE_ERR_WORKSPACE", 4: "MOE_ERR_CUDA", 5: "MOE_ERR_TIMEOUT",
                 6: "MOE_ERR_DEVICE_CHECK"}
-MOE_DTYPE_F32, MOE_DTYPE_BF16, MOE_DTYPE_E4M3, MOE_DTYPE_MXFP8 = 0, 1, 2, 3
+MOE_DTYPE_F32, MOE_DTYPE_BF16, MOE_DTYPE_E4M3, MOE_DTYPE_MXFP8, MOE_DTYPE_MXFP4 = 0, 1, 2, 3, 4
 MOE_TILE_AUTO, MOE_TILE_DECODE, MOE_TILE_PREFILL, MOE_TILE_MEDIUM = 0, 1, 2, 3
 MOE_FLAG_TEST_SKIP_SIGNAL = 0x1
 
@@ -29,7 +29,9 @@ EXPORTED = ("moe_workspace_size", "moe_router_logits", "moe_route", "moe_route_g
             "moe_get_workspace_layout", "moe_get_device_status", "moe_reset_device_status",
             "moe_status_string", "moe_down_combine_noalloc", "moe_quantize_rows_e4m3",
             "moe_forward_fp8", "moe_forward_single_launch", "moe_mx_scale_cols",
-            "moe_quantize_mx", "moe_forward_mx")
+            "moe_quantize_mx", "moe_forward_mx", "moe_mxfp4_code_cols", "moe_mxfp4_scale_bytes",
+            "moe_quantize_mxfp4", "moe_quantize_mxfp4_gate_up", "moe_dequantize_mxfp4",
+            "moe_linear_mxfp4_workspace_size", "moe_linear_mxfp4", "moe_forward_mxfp4")
 
 
 class MoEError(RuntimeError):
@@ -93,6 +95,15 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
             "moe_quantize_mx": [_P, ctypes.c_int32, _I64, _I64, _P, _P, _P],
             "moe_forward_mx": [pb, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P,
                                _P, _P, ctypes.c_size_t, _P],
+            "moe_quantize_mxfp4": [_P, ctypes.c_int32, _I64, _I64, _I64, _P, _P, _P],
+            "moe_quantize_mxfp4_gate_up": [_P, _P, ctypes.c_int32, _I64, _I64, _I64, _P, _P, _P],
+            "moe_dequantize_mxfp4": [_P, _P, _I64, _I64, _P, ctypes.c_int32, _I64, _P],
+            "moe_linear_mxfp4_workspace_size": [_I64, _I64, _I64, ctypes.c_int32,
+                                                ctypes.POINTER(ctypes.c_size_t)],
+            "moe_linear_mxfp4": [_P, _I64, _I64, _I64, ctypes.c_int32, _P, _P, _I64, _P,
+                                 ctypes.c_int32, _I64, _P, ctypes.c_size_t, _P],
+            "moe_forward_mxfp4": [pb, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P,
+                                  ctypes.c_size_t, _P],
             "moe_down_combine_noalloc": [pb, _P, _P, _P, _P, _P, _P, _P, _P, _P,
                                          ctypes.POINTER(ctypes.c_int)],
         }
@@ -102,6 +113,10 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
             f.restype = ctypes.c_int
         lib.moe_mx_scale_cols.argtypes = [_I64]
         lib.moe_mx_scale_cols.restype = _I64
+        lib.moe_mxfp4_code_cols.argtypes = [_I64]
+        lib.moe_mxfp4_code_cols.restype = _I64
+        lib.moe_mxfp4_scale_bytes.argtypes = [_I64, _I64]
+        lib.moe_mxfp4_scale_bytes.restype = _I64
         lib.moe_status_string.argtypes = [ctypes.c_int]
         lib.moe_status_string.restype = ctypes.c_char_p
         if path is None:
@@ -135,7 +150,8 @@ def make_problem(T, H, E, k, I, I_shared=0, renorm=1, dtype="bf16", tile=MOE_TIL
                  topk_group=1) -> MoEProblem:
     dt = (MOE_DTYPE_BF16 if dtype in ("bf16", torch.bfloat16)
           else MOE_DTYPE_E4M3 if dtype == "e4m3"
-          else MOE_DTYPE_MXFP8 if dtype == "mxfp8" else MOE_DTYPE_F32)
+          else MOE_DTYPE_MXFP8 if dtype == "mxfp8"
+          else MOE_DTYPE_MXFP4 if dtype == "mxfp4" else MOE_DTYPE_F32)
     return MoEProblem(T, H, E, k, I, I_shared, renorm, dt, tile, flags, wait_limit_us,
                       1 if out_f32 else 0, n_group, topk_group)
 
@@ -250,6 +266,102 @@ def forward_mx(problem, x, W_router, router_bias, Wq_gate, s_gate, Wq_up, s_up, 
         _ptr(s_gate), _ptr(Wq_up), _ptr(s_up), _ptr(Wq_down), _ptr(s_down), _ptr(Wsq_gate),
         _ptr(ss_gate), _ptr(Wsq_up), _ptr(ss_up), _ptr(Wsq_down), _ptr(ss_down), _ptr(y),
         _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def mxfp4_code_cols(cols: int) -> int:
+    """Bytes of a row of MXFP4 codes for `cols` elements (moe_mxfp4_code_cols)."""
+    return int(load_library().moe_mxfp4_code_cols(int(cols)))
+
+
+def mxfp4_scale_bytes(rows: int, cols: int) -> int:
+    """Bytes of the MXFP4 scales of a [rows, cols] matrix (moe_mxfp4_scale_bytes)."""
+    return int(load_library().moe_mxfp4_scale_bytes(int(rows), int(cols)))
+
+
+def _float_dtype(t, name: str) -> int:
+    """MOE_DTYPE of a bf16 or fp32 matrix whose rows are contiguous."""
+    if t.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"{name}: bf16 or fp32 expected, got {t.dtype}")
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name}: a matrix with contiguous rows expected")
+    return MOE_DTYPE_BF16 if t.dtype == torch.bfloat16 else MOE_DTYPE_F32
+
+
+def _row_stride(t) -> int:
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _check_mxfp4(q, scales, rows: int, cols: int, name: str):
+    """Codes and scales are contiguous bytes of the sizes [rows, cols] has."""
+    for t, n in ((q, rows * mxfp4_code_cols(cols)), (scales, mxfp4_scale_bytes(rows, cols))):
+        if t.dtype != torch.uint8 or not t.is_contiguous() or t.numel() != n:
+            raise ValueError(f"{name}: {n} contiguous bytes expected for [{rows}, {cols}], got "
+                             f"{t.numel()} of {t.dtype}")
+
+
+def quantize_mxfp4(src, q, scales, stream=None):
+    """MXFP4 codes q [rows, mxfp4_code_cols(cols)] and tiled scales
+    (mxfp4_scale_bytes(rows, cols) bytes) of src [rows, cols] (bf16 or fp32,
+    contiguous rows, any row stride), as moe_quantize_mxfp4 defines them."""
+    dt = _float_dtype(src, "src")
+    rows, cols = src.shape
+    _check_mxfp4(q, scales, rows, cols, "q, scales")
+    _check("moe_quantize_mxfp4", load_library().moe_quantize_mxfp4(
+        _ptr(src), dt, rows, cols, _row_stride(src), _ptr(q), _ptr(scales), _stream(stream)))
+
+
+def quantize_mxfp4_gate_up(W_gate, W_up, q, scales, stream=None):
+    """One MXFP4 matrix of E * 2I rows from W_gate, W_up [E, I, H] (gate and up
+    rows alternating in runs of 64), as moe_quantize_mxfp4_gate_up defines it."""
+    E, I, H = W_gate.shape
+    if W_up.shape != W_gate.shape or W_up.dtype != W_gate.dtype or not (
+            W_gate.is_contiguous() and W_up.is_contiguous()):
+        raise ValueError("W_gate, W_up: two contiguous tensors of one shape and dtype expected")
+    dt = _float_dtype(W_gate.view(E * I, H), "W_gate")
+    _check_mxfp4(q, scales, 2 * E * I, H, "q, scales")
+    _check("moe_quantize_mxfp4_gate_up", load_library().moe_quantize_mxfp4_gate_up(
+        _ptr(W_gate), _ptr(W_up), dt, E, I, H, _ptr(q), _ptr(scales), _stream(stream)))
+
+
+def dequantize_mxfp4(q, scales, out, stream=None):
+    """out [rows, cols] (bf16 or fp32, any row stride): the values of an MXFP4
+    matrix (moe_dequantize_mxfp4)."""
+    dt = _float_dtype(out, "out")
+    rows, cols = out.shape
+    _check_mxfp4(q, scales, rows, cols, "q, scales")
+    _check("moe_dequantize_mxfp4", load_library().moe_dequantize_mxfp4(
+        _ptr(q), _ptr(scales), rows, cols, _ptr(out), dt, _row_stride(out), _stream(stream)))
+
+
+def linear_mxfp4_workspace_size(T: int, N: int, K: int, act: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check("moe_linear_mxfp4_workspace_size", load_library().moe_linear_mxfp4_workspace_size(
+        T, N, K, act, ctypes.byref(n)))
+    return int(n.value)
+
+
+def linear_mxfp4(x, act: int, Wq, s_W, N: int, y, workspace, stream=None):
+    """y [T, N] (bf16 or fp32) = x [T, K] (bf16) times MXFP4 weights, x quantized
+    to `act` (MOE_DTYPE_MXFP8 or MOE_DTYPE_MXFP4), as moe_linear_mxfp4."""
+    if _float_dtype(x, "x") != MOE_DTYPE_BF16:
+        raise ValueError("x: bf16 expected")
+    dt = _float_dtype(y, "y")
+    T, K = x.shape
+    if tuple(y.shape) != (T, N):
+        raise ValueError(f"y: shape {(T, N)} expected, got {tuple(y.shape)}")
+    _check_mxfp4(Wq, s_W, N, K, "Wq, s_W")
+    _check("moe_linear_mxfp4", load_library().moe_linear_mxfp4(
+        _ptr(x), T, K, _row_stride(x), act, _ptr(Wq), _ptr(s_W), N, _ptr(y), dt, _row_stride(y),
+        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def forward_mxfp4(problem, x, W_router, router_bias, Wq_gate_up, s_gate_up, Wq_down, s_down,
+                  Wsq_gate_up, ss_gate_up, Wsq_down, ss_down, y, workspace, stream=None):
+    _check("moe_forward_mxfp4", load_library().moe_forward_mxfp4(
+        ctypes.byref(problem), _ptr(x), _ptr(W_router), _ptr(router_bias), _ptr(Wq_gate_up),
+        _ptr(s_gate_up), _ptr(Wq_down), _ptr(s_down), _ptr(Wsq_gate_up), _ptr(ss_gate_up),
+        _ptr(Wsq_down), _ptr(ss_down), _ptr(y), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
 def forward(problem, x, W_router, router_bias, W_gate, W_up, W_down, Ws_gate, Ws_up, Ws_down, y,

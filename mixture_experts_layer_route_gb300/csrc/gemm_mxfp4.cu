@@ -1,0 +1,848 @@
+// Products with MXFP4 weights on the block-scaled tensor-core MMA
+// (tcgen05.mma .block_scale): the MoE layer's gate/up and down GEMMs and the
+// dense product y = x W^T.
+//
+//   acc[m][n] = sum_b 2^(sA[m][b] + sB[n][b] - 254) sum_{k in block b} A[m][k] B[n][k]
+//
+// with A the weights' E2M1 codes, B the tokens' codes (E4M3, or E2M1 for the
+// dense product), sA and sB their E8M0 scale bytes per block of 32 along K.
+// The tensor cores multiply codes, apply both scales and accumulate in fp32:
+// nothing is expanded or rounded on the way.
+//
+// Orientation as in grouped_gemm.cuh: the weights are the MMA's M operand (128
+// rows a CTA), the tokens its N operand, so that ragged groups cost at most one
+// partly filled tile and a few tokens stream their weights with a narrow N.
+//
+// What the operands look like in shared memory (rows of 128 bytes, 128-byte
+// swizzle, K-major):
+//   E4M3 tokens: one k tile (128 elements) a stage. The weight codes are
+//     spread to one code a byte position by the TMA load itself (16 codes to 8
+//     bytes of data and 8 of padding, the form kind::mxf8f6f4 reads), so 8 KB
+//     from memory fill 16 KB of a stage.
+//   E2M1 tokens (kind::mxf4): both operands packed, two k tiles a stage.
+// Scales travel in groups of KG k tiles through a ring of their own (one box
+// of KG 512-byte tiles for the weights, one of KG x RA for the tokens) and
+// are copied into one of two column ranges of tensor memory by tcgen05.cp. An
+// MMA behind such a copy waits ~200 cycles for it, which is why a group spans
+// several stages: with copies before every stage of four MMAs (63 cycles
+// each, at N <= 128) they took 45% of the tensor pipe's time.
+//
+// Warp roles: warp 0 TMA producer, warp 1 MMA issuer (one thread) and owner of
+// the tensor memory, the others epilogue (four per group, one 32-lane quarter
+// each; groups take alternate 32-column chunks). Two accumulators let a unit's
+// epilogue run under the next unit's main loop. CL = 2: CTA pairs
+// (cta_group::2), each CTA with its own 128 weight rows and half of the token
+// rows, the leader issuing for both (see grouped_gemm.cuh). Every wait is
+// bounded (status word).
+#include <cstring>
+
+#include "grouped_gemm.cuh"
+#include "kernels.h"
+#include "mxfp4.cuh"
+
+namespace moe {
+
+namespace {
+
+enum Mx4Mode : int { kGatedMx4 = 0, kDownMx4 = 1, kLinearMx4 = 2 };
+
+struct Mx4Args {
+  // [0] routed, [1] shared group. B: boxes of B_ROWS, BOX1 and BOX2 rows.
+  CUtensorMap tmA[2], tmSA[2], tmB[2][3], tmSB[2];
+  const int32_t* offsets;     // [E+2] (GATED, DOWN)
+  const int32_t* gather_idx;  // [T*k] (DOWN)
+  const float* topk_w;        // [T*k] (DOWN)
+  // GATED: h codes by position; DOWN: Y fp32 [T][KP][H]; LINEAR: y [T][N], or
+  // fp32 partial sums [splits][T][N].
+  void* out;
+  uint8_t* out_s;             // GATED: scale tiles of h
+  void* out_shared;           // GATED: shared h codes by token, and their scale tiles
+  uint8_t* out_shared_s;
+  int* status;
+  unsigned long long limit_ns;
+  int T, k, E, KP;
+  int rows[2];                // weight rows per group (GATED: 2 I)
+  int kt[2];                  // k tiles (of 128) of the contraction
+  unsigned flags;
+  // LINEAR
+  int64_t ld_out;
+  int out_f32, splits, groups_per_split, vec_out;
+};
+
+template <int MODE, bool F4, int CL, int BN, int STAGES, int KG, int EG>
+struct Mx4Cfg {
+  static constexpr int KT_STAGE = F4 ? 2 : 1;          // k tiles per stage
+  static constexpr int SPG = KG / KT_STAGE;            // stages per scale group
+  static constexpr int RA = (BN + 127) / 128;          // 128-row scale tiles per token tile
+  static constexpr int A_BYTES = 128 * 128;
+  static constexpr int A_TX = F4 ? A_BYTES : A_BYTES / 2;  // bytes the load counts
+  static constexpr int B_ROWS = BN / CL;
+  static constexpr int BOX1 = B_ROWS > 64 ? 64 : 32;
+  static constexpr int BOX2 = B_ROWS > 64 ? 32 : 16;
+  static constexpr int N_UNIT = 16 * CL;
+  static constexpr int B_BYTES = B_ROWS * 128;
+  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+  static constexpr int SA_BYTES = KG * 512, SB_BYTES = KG * RA * 512;
+  static constexpr int SF_BYTES = SA_BYTES + SB_BYTES;
+  static constexpr int SF_STAGES = 3;
+  static constexpr int SF_COLS = KG * 4 + KG * RA * 4;
+  static constexpr int USED_COLS = 2 * BN + 2 * SF_COLS;
+  static constexpr int TMEM_COLS = USED_COLS <= 256 ? 256 : 512;
+  static constexpr int EPI_GROUPS = EG;
+  static constexpr int EPI_THREADS = 128 * EG;
+  static constexpr int THREADS = 64 + EPI_THREADS;
+  static constexpr int EPI_FLOATS = (MODE == kDownMx4 ? 0 : EG * 128 * 33) + 2 * BN;
+  // full, empty [STAGES]; sffull, sfempty [SF_STAGES]; tfull, tempty [2]; drain
+  static constexpr int NBARS = 2 * STAGES + 2 * SF_STAGES + 5;
+  static_assert(USED_COLS <= 512, "tensor memory");
+  static_assert(STAGE_BYTES % 1024 == 0 && KG % KT_STAGE == 0, "stage");
+
+  static size_t smem_bytes(int E) {
+    return 1024 + (size_t)STAGES * STAGE_BYTES + (size_t)SF_STAGES * SF_BYTES + EPI_FLOATS * 4 +
+           NBARS * 8 + 16 + (MODE == kLinearMx4 ? 0 : 3 * (size_t)(E + 2) * 4);
+  }
+};
+
+// Shared-memory descriptor of a 512-byte scale tile for the 32-lane x 128-bit
+// copy: no swizzle, groups of 8 rows (16 bytes each) 128 bytes apart.
+__device__ __forceinline__ uint64_t scale_tile_desc(uint32_t addr) {
+  return (uint64_t)((addr >> 4) & 0x3FFFu) | (uint64_t)(128u >> 4) << 32 | (uint64_t)1 << 46;
+}
+
+// One scale tile into four columns of tensor memory (of both CTAs of a pair,
+// each from its own shared memory), repeated over the four lane quarters.
+template <int CL>
+__device__ __forceinline__ void copy_scale_tile(uint32_t taddr, uint64_t desc) {
+  if constexpr (CL == 2)
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
+                 : "memory");
+  else
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
+                 : "memory");
+}
+
+// Instruction descriptor of the block-scaled kinds: operand formats at bits 7
+// and 10 (kind::mxf8f6f4: E4M3 0, E2M1 5; kind::mxf4: E2M1 1), N / 8 at bit
+// 17, E8M0 scales (bit 23), M / 16 at bit 24; the byte of a scale column that
+// holds the MMA's first block at bits 29 (A) and 4 (B).
+__device__ __forceinline__ uint32_t idesc_scaled(uint32_t fa, uint32_t fb, uint32_t M, uint32_t N,
+                                                 uint32_t sf) {
+  return (sf << 4) | (fa << 7) | (fb << 10) | ((N >> 3) << 17) | (1u << 23) | ((M >> 4) << 24) |
+         (sf << 29);
+}
+
+template <int CL, bool F4>
+__device__ __forceinline__ void mma_scaled(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                           uint32_t sa, uint32_t sb, uint32_t accumulate) {
+#define MOE_MMA_SCALED(group, kind, vec)                                                     \
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"                             \
+               "tcgen05.mma.cta_group::" group ".kind::" kind ".block_scale.scale_vec::" vec \
+               " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),                            \
+               "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)                 \
+               : "memory")
+  if constexpr (CL == 2 && F4) MOE_MMA_SCALED("2", "mxf4", "2X");
+  else if constexpr (CL == 2) MOE_MMA_SCALED("2", "mxf8f6f4", "1X");
+  else if constexpr (F4) MOE_MMA_SCALED("1", "mxf4", "2X");
+  else MOE_MMA_SCALED("1", "mxf8f6f4", "1X");
+#undef MOE_MMA_SCALED
+}
+
+// One unit of work of a CTA (pair): weight row block nb (of 128 rows; pairs
+// take 2 nb and 2 nb + 1) of group g on one token tile, over scale groups
+// [sg0, sg1) of the contraction.
+struct Mx4Tile {
+  int g, nb, p0, n_valid, sg0, sg1, split;
+  int64_t tb;  // scale tile of the token tile
+};
+
+template <int MODE, bool F4, int CL, int BN, int STAGES, int KG, int EG>
+__global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, KG, EG>::THREADS, 1)
+    mx4_gemm_kernel(const __grid_constant__ Mx4Args args) {
+  pdl_trigger();
+  using C = Mx4Cfg<MODE, F4, CL, BN, STAGES, KG, EG>;
+  constexpr bool PAIR = CL == 2;
+  constexpr bool GROUPED = MODE != kLinearMx4;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  uint8_t* stages = smem;
+  uint8_t* sfs = stages + (size_t)STAGES * C::STAGE_BYTES;
+  float* epi = reinterpret_cast<float*>(sfs + (size_t)C::SF_STAGES * C::SF_BYTES);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(epi + C::EPI_FLOATS);
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + C::NBARS);
+  volatile int* epi_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+  int* n_sched = reinterpret_cast<int*>(tmem_holder + 2);
+  int* n_heavy = reinterpret_cast<int*>(tmem_holder + 3);
+  int32_t* prefix = reinterpret_cast<int32_t*>(tmem_holder + 4);
+  int32_t* offs = prefix + (args.E + 2);
+  int32_t* order = offs + (args.E + 2);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int E = args.E;
+  const int crank = PAIR ? (int)cluster_ctarank() : 0;
+  const bool leader = crank == 0;
+  const int cid = blockIdx.x / CL, ncl = gridDim.x / CL;
+  const uint32_t bars_base = smem_u32(bars);
+  auto bar = [&](int i) { return bars_base + 8u * (uint32_t)i; };
+  auto full_bar = [&](int s) { return bar(s); };
+  auto empty_bar = [&](int s) { return bar(STAGES + s); };
+  auto sffull_bar = [&](int s) { return bar(2 * STAGES + s); };
+  auto sfempty_bar = [&](int s) { return bar(2 * STAGES + C::SF_STAGES + s); };
+  constexpr int B0 = 2 * STAGES + 2 * C::SF_STAGES;
+  auto tfull_bar = [&](int a) { return bar(B0 + a); };
+  auto tempty_bar = [&](int a) { return bar(B0 + 2 + a); };
+  const uint32_t drain_bar = bar(B0 + 4);
+  const uint32_t stages_base = smem_u32(stages), sfs_base = smem_u32(sfs);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < B0; ++s) mbar_init(bar(s), 1);
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(tfull_bar(a), 1);
+      mbar_init(tempty_bar(a), CL);
+    }
+    mbar_init(drain_bar, 1);
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane < 2) {
+    tma_prefetch_desc(&args.tmA[lane]);
+    tma_prefetch_desc(&args.tmSA[lane]);
+    tma_prefetch_desc(&args.tmSB[lane]);
+    for (int i = 0; i < 3; ++i) tma_prefetch_desc(&args.tmB[lane][i]);
+  }
+  if (warp == 1) {
+    if constexpr (PAIR)
+      tmem_alloc_pair(smem_u32(tmem_holder), C::TMEM_COLS);
+    else
+      tmem_alloc(smem_u32(tmem_holder), C::TMEM_COLS);
+  }
+  pdl_wait();  // global memory from here on
+  if constexpr (GROUPED) {
+    if (warp == 2)
+      build_schedule<128 * CL>(args.offsets, E, args.T, args.k, args.KP, 1, 1 << 30, BN,
+                               (args.rows[0] + 128 * CL - 1) / (128 * CL) * (128 * CL),
+                               (args.rows[1] + 128 * CL - 1) / (128 * CL) * (128 * CL),
+                               args.status, offs, order, prefix, n_sched, n_heavy, lane);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if constexpr (PAIR) cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_holder;
+  const uint32_t sf_cols = tmem_base + 2 * BN;
+  const uint64_t limit = args.limit_ns;
+
+  int ngroups = 0, heavy_units = 0, total;
+  int lin_nb = 0, lin_mt = 0;
+  if constexpr (GROUPED) {
+    ngroups = *n_sched;
+    heavy_units = *n_heavy;
+    total = prefix[ngroups];
+  } else {
+    lin_nb = (args.rows[0] + 128 * CL - 1) / (128 * CL);
+    lin_mt = (args.T + BN - 1) / BN;
+    total = lin_nb * lin_mt * args.splits;
+  }
+  auto tile_of = [&](int u) {
+    Mx4Tile t;
+    int m, mt;
+    if constexpr (GROUPED) {
+      const Tile tl =
+          decode_tile(remap_unit(u, total, heavy_units), prefix, order, offs, ngroups, BN);
+      t.g = tl.g;
+      t.nb = tl.nb * CL + crank;
+      mt = tl.mt;
+      m = offs[tl.g + 1] - offs[tl.g];
+      t.tb = tl.g == E ? 0 : group_scale_tile(offs[tl.g], tl.g, BN);
+      t.p0 = tl.g == E ? 0 : offs[tl.g];  // the shared group's rows are in token order
+      t.sg0 = 0;
+      t.sg1 = (args.kt[tl.g == E] + KG - 1) / KG;
+      t.split = 0;
+    } else {
+      // Token tiles fastest, so that the CTAs at work share weight rows in L2.
+      t.g = 0;
+      mt = u % lin_mt;
+      const int v = u / lin_mt;
+      t.nb = (v % lin_nb) * CL + crank;
+      t.split = v / lin_nb;
+      m = args.T;
+      t.tb = 0;
+      t.p0 = 0;
+      const int sg = (args.kt[0] + KG - 1) / KG;
+      t.sg0 = t.split * args.groups_per_split;
+      t.sg1 = min(sg, t.sg0 + args.groups_per_split);
+    }
+    const int tn = token_tile_rows(m, BN, C::N_UNIT);
+    t.tb += mt;
+    t.p0 += mt * tn;
+    t.n_valid = min(tn, m - mt * tn);
+    return t;
+  };
+  auto mma_cols = [&](const Mx4Tile& t) {
+    return (t.n_valid + C::N_UNIT - 1) / C::N_UNIT * C::N_UNIT;
+  };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    const uint64_t pol_w = PAIR ? l2_policy_evict_normal() : l2_policy_evict_first();
+    const uint64_t pol_t = l2_policy_evict_last();
+    // Test hook: the first stage is neither signalled nor loaded, so that the
+    // MMA issuer's wait on it runs out.
+    const bool skip_first = (args.flags & MOE_FLAG_TEST_SKIP_SIGNAL) != 0;
+    bool skip = skip_first;
+    uint32_t it = 0, sit = 0;
+    bool ok = true;
+    for (int u = cid; u < total && ok; u += ncl) {
+      const Mx4Tile t = tile_of(u);
+      const int sh = GROUPED && t.g == E ? 1 : 0;
+      const int kt = args.kt[sh];
+      // The last row block of a pair may lie past the group's rows: it loads
+      // what is there (another group's rows, or zeros) and stores nothing.
+      const int rt = (sh || !GROUPED ? 0 : t.g * (args.rows[0] / 128)) + t.nb;
+      const int need = mma_cols(t) / CL;
+      const int bsel = need <= C::BOX2 ? 2 : (need <= C::BOX1 ? 1 : 0);
+      const int box = bsel == 2 ? C::BOX2 : (bsel == 1 ? C::BOX1 : C::B_ROWS);
+      const uint32_t tx = CL * (C::A_TX + box * 128);
+      // Lane 0 loads the weights, lane 1 the tokens.
+      const CUtensorMap* my_map = lane == 0 ? &args.tmA[sh] : &args.tmB[sh][bsel];
+      const int my_row = lane == 0 ? rt * 128 : t.p0 + crank * need;
+      const uint32_t my_off = lane == 0 ? 0u : (uint32_t)C::A_BYTES;
+      const uint64_t my_pol = lane == 0 ? pol_w : pol_t;
+      // Elements (E2M1 spread by the load) or bytes a stage along the row.
+      const CUtensorMap* my_smap = lane == 0 ? &args.tmSA[sh] : &args.tmSB[sh];
+      const int64_t s_row0 = lane == 0 ? (int64_t)rt * kt : t.tb * kt * C::RA;
+      const int s_step = lane == 0 ? 1 : C::RA;
+      const uint32_t s_off = lane == 0 ? 0u : (uint32_t)C::SA_BYTES;
+      for (int sg = t.sg0; sg < t.sg1 && ok; ++sg) {
+        {
+          const int s = (int)(sit % C::SF_STAGES);
+          int wok = 1;
+          if (lane == 0)
+            wok = mbar_wait(sfempty_bar(s), ((sit / C::SF_STAGES) & 1u) ^ 1u, args.status, limit);
+          if (!__shfl_sync(0xffffffffu, wok, 0)) {
+            ok = false;
+            break;
+          }
+          ++sit;
+          const uint32_t dst = sfs_base + (uint32_t)(s * C::SF_BYTES) + s_off;
+          if (leader && lane == 0)
+            mbar_arrive_expect_tx(sffull_bar(s), (uint32_t)(CL * C::SF_BYTES));
+          __syncwarp();
+          if (lane < 2) {
+            const int y = (int)(s_row0 + (int64_t)sg * KG * s_step);
+            if constexpr (PAIR)
+              tma_load_2d_pair(dst, my_smap, 0, y, mapa_shared(sffull_bar(s), 0), my_pol);
+            else
+              tma_load_2d(dst, my_smap, 0, y, sffull_bar(s), my_pol);
+          }
+        }
+        const int kend = min(kt, (sg + 1) * KG);
+        for (int ks = sg * KG; ks < kend; ks += C::KT_STAGE) {
+          const int s = (int)(it % STAGES);
+          int wok = 1;
+          if (lane == 0)
+            wok = mbar_wait(empty_bar(s), ((it / STAGES) & 1u) ^ 1u, args.status, limit);
+          if (!__shfl_sync(0xffffffffu, wok, 0)) {
+            ok = false;
+            break;
+          }
+          ++it;
+          if (skip) {
+            skip = false;
+            continue;
+          }
+          const uint32_t dst = stages_base + (uint32_t)s * C::STAGE_BYTES + my_off;
+          if (leader && lane == 0) mbar_arrive_expect_tx(full_bar(s), tx);
+          __syncwarp();
+          if (lane < 2) {
+            const int x = F4 ? ks * 64 : ks * 128;
+            if constexpr (PAIR)
+              tma_load_2d_pair(dst, my_map, x, my_row, mapa_shared(full_bar(s), 0), my_pol);
+            else
+              tma_load_2d(dst, my_map, x, my_row, full_bar(s), my_pol);
+          }
+        }
+      }
+    }
+    // Let the last loads land before the CTA (pair) can exit.
+    if (lane == 0 && leader) {
+      const uint32_t n = it < (uint32_t)STAGES ? it : (uint32_t)STAGES;
+      for (uint32_t i = it - n; i < it; ++i) {
+        if (skip_first && i == 0) continue;  // never loaded
+        mbar_wait(full_bar((int)(i % STAGES)), (i / STAGES) & 1u, nullptr, 20000000ull);
+      }
+      const uint32_t m = sit < (uint32_t)C::SF_STAGES ? sit : (uint32_t)C::SF_STAGES;
+      for (uint32_t i = sit - m; i < sit; ++i)
+        mbar_wait(sffull_bar((int)(i % C::SF_STAGES)), (i / C::SF_STAGES) & 1u, nullptr,
+                  20000000ull);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0 && leader) {
+      uint32_t it = 0, sit = 0, lt = 0;
+      bool ok = true;
+      for (int u = cid; u < total && ok; u += ncl, ++lt) {
+        const Mx4Tile t = tile_of(u);
+        const int kt = args.kt[GROUPED && t.g == E ? 1 : 0];
+        const uint32_t acc = lt & 1u;
+        if (!mbar_wait(tempty_bar(acc), ((lt >> 1) & 1u) ^ 1u, args.status, limit)) break;
+        tc_fence_after();
+        const uint32_t d = tmem_base + acc * BN;
+        uint32_t idesc[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          idesc[i] = F4 ? idesc_scaled(1, 1, 128 * CL, (uint32_t)mma_cols(t), (i & 1) * 2)
+                        : idesc_scaled(5, 0, 128 * CL, (uint32_t)mma_cols(t), i);
+        uint32_t accumulate = 0;
+        for (int sg = t.sg0; sg < t.sg1 && ok; ++sg, ++sit) {
+          const int ss = (int)(sit % C::SF_STAGES);
+          if (!mbar_wait(sffull_bar(ss), (sit / C::SF_STAGES) & 1u, args.status, limit)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = sf_cols + (sit & 1u) * C::SF_COLS, sb = sa + KG * 4;
+          const uint32_t src = sfs_base + (uint32_t)(ss * C::SF_BYTES);
+          const int nk = min(KG, kt - sg * KG);
+          for (int i = 0; i < nk; ++i) copy_scale_tile<CL>(sa + i * 4, scale_tile_desc(src + i * 512));
+          for (int i = 0; i < nk * C::RA; ++i)
+            copy_scale_tile<CL>(sb + i * 4, scale_tile_desc(src + C::SA_BYTES + i * 512));
+          if constexpr (PAIR)
+            umma_commit_pair_multicast(sfempty_bar(ss), 0x3);
+          else
+            umma_commit(sfempty_bar(ss));
+          for (int i0 = 0; i0 < nk; i0 += C::KT_STAGE, ++it) {
+            const int s = (int)(it % STAGES);
+            if (!mbar_wait(full_bar(s), (it / STAGES) & 1u, args.status, limit)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t a_addr = stages_base + (uint32_t)s * C::STAGE_BYTES;
+            const uint32_t b_addr = a_addr + C::A_BYTES;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int kti = i0 + (F4 ? i >> 1 : 0);  // this MMA's k tile in the group
+              if (F4 && kti >= nk) break;              // an odd last k tile: half a stage
+              mma_scaled<CL, F4>(d, umma_desc_sw128(a_addr + i * 32),
+                                 umma_desc_sw128(b_addr + i * 32), idesc[i], sa + kti * 4,
+                                 sb + kti * 4 * C::RA, accumulate);
+              accumulate = 1;
+            }
+            if constexpr (PAIR)
+              umma_commit_pair_multicast(empty_bar(s), 0x3);
+            else
+              umma_commit(empty_bar(s));
+          }
+        }
+        if (!ok) break;
+        if constexpr (PAIR)
+          umma_commit_pair_multicast(tfull_bar(acc), 0x3);
+        else
+          umma_commit(tfull_bar(acc));
+      }
+      if constexpr (PAIR)
+        umma_commit_pair(drain_bar);
+      else
+        umma_commit(drain_bar);
+      mbar_wait(drain_bar, 0, nullptr, 20000000ull);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int q = warp & 3;               // tensor-memory lane quarter
+    const int eg = (warp - 2) >> 2;       // chunk group
+    const int et = threadIdx.x - 64;      // 0..EPI_THREADS-1
+    const int gt = et & 127;              // thread of the group
+    const uint32_t lane_base = (uint32_t)(q * 32) << 16;
+    int32_t* yrow = reinterpret_cast<int32_t*>(epi);
+    float* wt = epi + BN;
+    float* stage = epi + 2 * BN + eg * 128 * 33;  // [128][33], this group's
+    uint32_t lt = 0;
+    for (int u = cid; u < total; u += ncl, ++lt) {
+      const Mx4Tile t = tile_of(u);
+      const bool shared = GROUPED && t.g == E;
+      const uint32_t acc = lt & 1u;
+      if (et == 0) *epi_flag = mbar_wait(tfull_bar(acc), (lt >> 1) & 1u, args.status, limit) ? 1 : 0;
+      if constexpr (MODE == kDownMx4) {
+        // Destination row in Y and gate weight of each column.
+        for (int j = et; j < t.n_valid; j += C::EPI_THREADS) {
+          int row;
+          float wv;
+          if (shared) {
+            row = (t.p0 + j) * args.KP + args.k;
+            wv = 1.0f;
+          } else {
+            const int s = args.gather_idx[t.p0 + j];
+            if ((unsigned)s < (unsigned)(args.T * args.k)) {
+              const int tok = s / args.k;
+              row = tok * args.KP + (s - tok * args.k);
+              wv = args.topk_w[s];
+            } else {  // device check: reported; the column goes to row 0 as zeros
+              set_status(args.status, MOE_ERR_DEVICE_CHECK);
+              row = 0;
+              wv = 0.f;
+            }
+          }
+          yrow[j] = row;
+          wt[j] = wv;
+        }
+      }
+      named_barrier_sync(1, C::EPI_THREADS);
+      if (!*epi_flag) break;  // every epilogue thread sees the same flag
+      tc_fence_after();
+      const uint32_t t_acc = tmem_base + lane_base + acc * BN;
+      const bool live = t.nb * 128 < args.rows[shared];  // a pair's block past the last one
+      if constexpr (MODE == kDownMx4) {
+        // Thread = output feature; a warp stores 32 consecutive floats of a
+        // token's slot row per column.
+        const size_t H = (size_t)args.rows[0];
+        float* Yc = reinterpret_cast<float*>(args.out) + (size_t)t.nb * 128 + q * 32 + lane;
+        const int4* yrow4 = reinterpret_cast<const int4*>(yrow);
+        const float4* wt4 = reinterpret_cast<const float4*>(wt);
+        for (int c0 = 32 * eg; live && c0 < t.n_valid; c0 += 32 * EG) {
+          float v[32];
+          tmem_ld32(t_acc + c0, v);
+          const int nj = min(32, t.n_valid - c0);
+#pragma unroll
+          for (int i4 = 0; i4 < 8; ++i4) {
+            const int4 r = yrow4[(c0 >> 2) + i4];
+            const float4 wv = wt4[(c0 >> 2) + i4];
+            const int i = 4 * i4;
+            if (i + 3 < nj) {
+              Yc[(size_t)r.x * H] = wv.x * v[i];
+              Yc[(size_t)r.y * H] = wv.y * v[i + 1];
+              Yc[(size_t)r.z * H] = wv.z * v[i + 2];
+              Yc[(size_t)r.w * H] = wv.w * v[i + 3];
+            } else {
+              if (i < nj) Yc[(size_t)r.x * H] = wv.x * v[i];
+              if (i + 1 < nj) Yc[(size_t)r.y * H] = wv.y * v[i + 1];
+              if (i + 2 < nj) Yc[(size_t)r.z * H] = wv.z * v[i + 2];
+            }
+          }
+        }
+      } else {
+        // 32 columns at a time through shared memory: lanes hold weight rows,
+        // and both epilogues want several rows of one token in a thread.
+        // Thread: token column jj, rows 8 fg + 0..7 of each 32-row block (a
+        // warp's eight tokens and four row groups fall on 32 distinct banks).
+        const int jj = gt >> 2, fg = gt & 3;
+        for (int c0 = 32 * eg; live && c0 < t.n_valid; c0 += 32 * EG) {
+          float v[32];
+          tmem_ld32(t_acc + c0, v);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) stage[(q * 32 + lane) * 33 + i] = v[i];
+          named_barrier_sync(2 + eg, 128);
+          const int j = c0 + jj;
+          if constexpr (MODE == kGatedMx4) {
+            // Rows 0..63 are gate, 64..127 up, of features 64 nb ..; h is
+            // quantized from fp32 per 32 features (the four threads of a token
+            // hold a block).
+            const int kt_out = args.rows[shared] / 256;  // I / 128
+            uint32_t bytes[2];
+            uint2 codes[2];
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              float hv[8];
+              uint32_t amax = 0;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float g = stage[(b * 32 + fg * 8 + i) * 33 + jj];
+                const float up = stage[(64 + b * 32 + fg * 8 + i) * 33 + jj];
+                // silu(g) * up; approximate exp and divide (a few ulp of fp32,
+                // far below the E4M3 rounding that follows).
+                hv[i] = __fdividef(g, 1.0f + __expf(-g)) * up;
+                amax = max(amax, __float_as_uint(hv[i]) & 0x7FFFFFFFu);
+              }
+              amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+              amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+              bytes[b] = mx_scale_byte(amax, 8);
+              const float inv = mx_inv_scale(bytes[b]);
+              codes[b] = make_uint2(mx_encode4(mx_scaled(hv[0], inv), mx_scaled(hv[1], inv),
+                                               mx_scaled(hv[2], inv), mx_scaled(hv[3], inv)),
+                                    mx_encode4(mx_scaled(hv[4], inv), mx_scaled(hv[5], inv),
+                                               mx_scaled(hv[6], inv), mx_scaled(hv[7], inv)));
+            }
+            if (j < t.n_valid) {
+              uint8_t* out = reinterpret_cast<uint8_t*>(shared ? args.out_shared : args.out);
+              uint8_t* osc = shared ? args.out_shared_s : args.out_s;
+              uint8_t* dst = out + (size_t)(t.p0 + j) * (kt_out * 128) + t.nb * 64 + fg * 8;
+              *reinterpret_cast<uint2*>(dst) = codes[0];
+              *reinterpret_cast<uint2*>(dst + 32) = codes[1];
+              // Features 64 nb: k tile nb / 2, blocks 0,1 or 2,3 of it.
+              if (fg == 0)
+                *reinterpret_cast<uint16_t*>(
+                    osc + ((t.tb * kt_out + (t.nb >> 1)) * C::RA + (j >> 7)) * 512 +
+                    mxfp4_scale_word((uint32_t)(j & 127)) + (t.nb & 1) * 2) =
+                    (uint16_t)(bytes[0] | (bytes[1] << 8));
+            }
+          } else {
+            const int N = args.rows[0];
+            if (j < t.n_valid) {
+              const int64_t row = (int64_t)t.split * args.T + t.p0 + j;
+#pragma unroll
+              for (int b = 0; b < 4; ++b) {
+                const int n0 = t.nb * 128 + b * 32 + fg * 8;
+                float o[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) o[i] = stage[(b * 32 + fg * 8 + i) * 33 + jj];
+                if (args.out_f32) {
+                  float* dst = reinterpret_cast<float*>(args.out) + row * args.ld_out + n0;
+                  if (args.vec_out && n0 + 8 <= N) {
+                    reinterpret_cast<float4*>(dst)[0] = make_float4(o[0], o[1], o[2], o[3]);
+                    reinterpret_cast<float4*>(dst)[1] = make_float4(o[4], o[5], o[6], o[7]);
+                  } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                      if (n0 + i < N) dst[i] = o[i];
+                  }
+                } else {
+                  __nv_bfloat16* dst =
+                      reinterpret_cast<__nv_bfloat16*>(args.out) + row * args.ld_out + n0;
+                  if (args.vec_out && n0 + 8 <= N) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                      const __nv_bfloat162 p = __floats2bfloat162_rn(o[2 * i], o[2 * i + 1]);
+                      w[i] = *reinterpret_cast<const uint32_t*>(&p);
+                    }
+                    *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+                  } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                      if (n0 + i < N) dst[i] = __float2bfloat16_rn(o[i]);
+                  }
+                }
+              }
+            }
+          }
+          named_barrier_sync(2 + eg, 128);
+        }
+      }
+      tc_fence_before();
+      named_barrier_sync(1, C::EPI_THREADS);
+      // The accumulator goes back to the issuer (its reads completed above).
+      if (et == 0) {
+        if constexpr (PAIR)
+          mbar_arrive_relaxed_cluster(mapa_shared(tempty_bar(acc), 0));
+        else
+          mbar_arrive_relaxed(tempty_bar(acc));
+      }
+    }
+  }
+
+  tc_fence_before();
+  if constexpr (PAIR)
+    cluster_sync();
+  else
+    __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    if constexpr (PAIR)
+      tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
+    else
+      tmem_dealloc(tmem_base, C::TMEM_COLS);
+  }
+}
+
+// y[t][n] = sum over the splits of the partial sums, in split order.
+template <typename TOut>
+__global__ void __launch_bounds__(256) split_sum_kernel(const float* __restrict__ part, int T,
+                                                        int N, int splits, TOut* __restrict__ y,
+                                                        int64_t ld) {
+  pdl_entry();
+  const int64_t n = (int64_t)T * N;
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n;
+       i += (int64_t)gridDim.x * blockDim.x) {
+    float s = part[i];
+    for (int k = 1; k < splits; ++k) s += part[i + k * n];
+    const int64_t t = i / N;
+    if constexpr (sizeof(TOut) == 2)
+      y[t * ld + (i - t * N)] = __float2bfloat16_rn(s);
+    else
+      y[t * ld + (i - t * N)] = s;
+  }
+}
+
+constexpr int kMaxExperts = 1024;  // the C ABI's limit on E
+constexpr int kSmallTile = 64;
+
+template <int MODE, bool F4, int CL, int BN, int STAGES, int KG, int EG>
+cudaError_t launch_variant(const Mx4Args& a, int num_sms, size_t units, cudaStream_t st) {
+  using C = Mx4Cfg<MODE, F4, CL, BN, STAGES, KG, EG>;
+  static_assert(CL == 1 || CL == 2, "single CTAs or pairs");
+  auto fn = mx4_gemm_kernel<MODE, F4, CL, BN, STAGES, KG, EG>;
+  cudaError_t e = ensure_smem_attr((const void*)fn, C::smem_bytes(kMaxExperts));
+  if (e != cudaSuccess) return e;
+  size_t n = (size_t)(num_sms / CL);
+  if (units < n) n = units;
+  if (n == 0) return cudaSuccess;
+  return launch_chained(fn, dim3((unsigned)(n * CL)), dim3(C::THREADS), C::smem_bytes(a.E), st,
+                        CL, a);
+}
+
+// Decode-sized batches: 64-row token tiles on single CTAs; otherwise 224-row
+// tiles on pairs.
+template <int MODE, bool F4>
+cudaError_t launch_mx4(const Mx4Args& a, bool wide, int num_sms, size_t units, cudaStream_t st) {
+  (void)wide;
+  return launch_variant<MODE, F4, 1, kSmallTile, 7, 4, 1>(a, num_sms, units, st);
+}
+
+struct TokenMaps {
+  const uint8_t *q, *s;
+  uint64_t rows;
+  int kt;
+  uint64_t tiles;  // token tiles of the scales
+};
+
+template <bool F4, int CL, int BN, int KG>
+bool make_token_maps(CUtensorMap (&m)[3], CUtensorMap* ms, const TokenMaps& t) {
+  using C = Mx4Cfg<kDownMx4, F4, CL, BN, 4, KG, 1>;
+  const uint64_t cols = (uint64_t)t.kt * (F4 ? 64 : 128);
+  return make_tma_map(&m[0], t.q, MOE_DTYPE_E4M3, t.rows, cols, C::B_ROWS) &&
+         make_tma_map(&m[1], t.q, MOE_DTYPE_E4M3, t.rows, cols, C::BOX1) &&
+         make_tma_map(&m[2], t.q, MOE_DTYPE_E4M3, t.rows, cols, C::BOX2) &&
+         make_scale_tile_map(ms, t.s, t.tiles * t.kt * C::RA, KG * C::RA);
+}
+
+template <bool F4, int KG>
+bool make_weight_maps(CUtensorMap* m, CUtensorMap* ms, const uint8_t* q, const uint8_t* s,
+                      uint64_t rows, int kt) {
+  const bool ok = F4 ? make_tma_map(m, q, MOE_DTYPE_E4M3, rows, (uint64_t)kt * 64, 128)
+                     : make_spread_code_map(m, q, rows, (uint64_t)kt * 128, 128);
+  return ok && make_scale_tile_map(ms, s, (rows + 127) / 128 * kt, KG);
+}
+
+}  // namespace
+
+Mx4Tiling mx4_tiling(int64_t T, int tile) {
+  (void)T;
+  (void)tile;
+  return {false, kSmallTile, 16, 1};
+}
+
+namespace {
+
+template <int MODE>
+cudaError_t launch_grouped(const GemmProblem& p, const Mx4Weights& w, const Mx4Tokens& x,
+                           const int32_t* offsets, const int32_t* gather_idx, const float* topk_w,
+                           const Mx4Out& out, float* Y, int* status, cudaStream_t st) {
+  constexpr bool GATED = MODE == kGatedMx4;
+  constexpr int KG = 4;
+  const bool has_s = p.Is > 0;
+  Mx4Args a;
+  memset(&a, 0, sizeof(a));
+  a.kt[0] = (GATED ? p.H : p.I) / 128;
+  a.kt[1] = GATED || !has_s ? a.kt[0] : p.Is / 128;
+  a.rows[0] = GATED ? 2 * p.I : p.H;
+  a.rows[1] = GATED ? (has_s ? 2 * p.Is : 2 * p.I) : p.H;
+  const int P = p.T * p.k;
+  const int bn = mx4_tiling(p.T, p.tile).rows;
+  const TokenMaps rt = {x.routed, x.routed_s, (uint64_t)P, a.kt[0],
+                        (uint64_t)group_scale_tile(P, p.E, bn) + 1};
+  const TokenMaps sh = {x.shared, x.shared_s, (uint64_t)p.T, a.kt[1],
+                        (uint64_t)((p.T + bn - 1) / bn)};
+  bool ok = make_weight_maps<false, KG>(&a.tmA[0], &a.tmSA[0], GATED ? w.gate_up : w.down,
+                                        GATED ? w.s_gate_up : w.s_down,
+                                        (uint64_t)p.E * a.rows[0], a.kt[0]) &&
+            make_token_maps<false, 1, kSmallTile, KG>(a.tmB[0], &a.tmSB[0], rt);
+  if (ok && has_s)
+    ok = make_weight_maps<false, KG>(&a.tmA[1], &a.tmSA[1], GATED ? w.sh_gate_up : w.sh_down,
+                                     GATED ? w.sh_s_gate_up : w.sh_s_down, (uint64_t)a.rows[1],
+                                     a.kt[1]) &&
+         make_token_maps<false, 1, kSmallTile, KG>(a.tmB[1], &a.tmSB[1], sh);
+  if (!ok) return cudaErrorInvalidValue;
+  if (!has_s) {
+    a.tmA[1] = a.tmA[0];
+    a.tmSA[1] = a.tmSA[0];
+    a.tmSB[1] = a.tmSB[0];
+    for (int i = 0; i < 3; ++i) a.tmB[1][i] = a.tmB[0][i];
+  }
+  a.offsets = offsets;
+  a.gather_idx = gather_idx;
+  a.topk_w = topk_w;
+  a.out = GATED ? (void*)out.routed : (void*)Y;
+  a.out_s = out.routed_s;
+  a.out_shared = out.shared;
+  a.out_shared_s = out.shared_s;
+  a.status = status;
+  a.limit_ns = p.limit_ns;
+  a.T = p.T;
+  a.k = p.k;
+  a.E = p.E;
+  a.KP = p.k + (has_s ? 1 : 0);
+  a.flags = p.flags;
+  const size_t ub = unit_upper_bound(p.T, p.k, p.E, bn, (a.rows[0] + 127) / 128,
+                                     has_s ? (a.rows[1] + 127) / 128 : 0);
+  return launch_mx4<MODE, false>(a, false, p.num_sms, ub, st);
+}
+
+}  // namespace
+
+cudaError_t launch_mx4_swiglu_gemm(const GemmProblem& p, const Mx4Weights& w, const Mx4Tokens& x,
+                                   const int32_t* offsets, const Mx4Out& h, int* status,
+                                   cudaStream_t st) {
+  return launch_grouped<kGatedMx4>(p, w, x, offsets, nullptr, nullptr, h, nullptr, status, st);
+}
+
+cudaError_t launch_mx4_down_gemm(const GemmProblem& p, const Mx4Weights& w, const Mx4Tokens& h,
+                                 const int32_t* offsets, const int32_t* gather_idx,
+                                 const float* topk_w, float* Y, int* status, cudaStream_t st) {
+  return launch_grouped<kDownMx4>(p, w, h, offsets, gather_idx, topk_w, Mx4Out{}, Y, status, st);
+}
+
+int mx4_linear_splits(int T, int64_t N, int64_t K, int num_sms) {
+  (void)T;
+  (void)N;
+  (void)K;
+  (void)num_sms;
+  return 1;
+}
+
+cudaError_t launch_mx4_linear(const Mx4Linear& l, cudaStream_t st) {
+  constexpr int KG = 4;
+  Mx4Args a;
+  memset(&a, 0, sizeof(a));
+  a.kt[0] = a.kt[1] = (int)mxfp4_k_tiles(l.K);
+  a.rows[0] = a.rows[1] = (int)l.N;
+  const int bn = mx4_tiling(l.T, MOE_TILE_AUTO).rows;
+  const TokenMaps tm = {l.xq, l.xs, (uint64_t)l.T, a.kt[0], (uint64_t)((l.T + bn - 1) / bn)};
+  const bool ok =
+      l.e2m1 ? make_weight_maps<true, KG>(&a.tmA[0], &a.tmSA[0], l.wq, l.ws, l.N, a.kt[0]) &&
+                   make_token_maps<true, 1, kSmallTile, KG>(a.tmB[0], &a.tmSB[0], tm)
+             : make_weight_maps<false, KG>(&a.tmA[0], &a.tmSA[0], l.wq, l.ws, l.N, a.kt[0]) &&
+                   make_token_maps<false, 1, kSmallTile, KG>(a.tmB[0], &a.tmSB[0], tm);
+  if (!ok) return cudaErrorInvalidValue;
+  a.tmA[1] = a.tmA[0];
+  a.tmSA[1] = a.tmSA[0];
+  a.tmSB[1] = a.tmSB[0];
+  for (int i = 0; i < 3; ++i) a.tmB[1][i] = a.tmB[0][i];
+  a.status = l.status;
+  a.limit_ns = l.limit_ns;
+  a.T = l.T;
+  a.splits = l.splits;
+  const int sg = (a.kt[0] + KG - 1) / KG;
+  a.groups_per_split = (sg + l.splits - 1) / l.splits;
+  a.splits = (sg + a.groups_per_split - 1) / a.groups_per_split;  // no empty split
+  const bool part = a.splits > 1;
+  a.out = part ? (void*)l.part : l.y;
+  a.ld_out = part ? l.N : l.ld_y;
+  a.out_f32 = part || l.y_f32;
+  const int es = a.out_f32 ? 4 : 2;
+  a.vec_out = (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0 && a.ld_out * es % 16 == 0;
+  const size_t units = (size_t)((l.N + 127) / 128) * ((l.T + bn - 1) / bn) * a.splits;
+  cudaError_t e = l.e2m1 ? launch_mx4<kLinearMx4, true>(a, false, l.num_sms, units, st)
+                         : launch_mx4<kLinearMx4, false>(a, false, l.num_sms, units, st);
+  if (e != cudaSuccess || !part) return e;
+  int64_t blocks = ((int64_t)l.T * l.N + 255) / 256;
+  if (blocks > 8 * (int64_t)l.num_sms) blocks = 8 * (int64_t)l.num_sms;
+  if (l.y_f32)
+    return launch_chained(split_sum_kernel<float>, dim3((unsigned)blocks), dim3(256), 0, st, 1,
+                          (const float*)l.part, l.T, (int)l.N, a.splits, (float*)l.y, l.ld_y);
+  return launch_chained(split_sum_kernel<__nv_bfloat16>, dim3((unsigned)blocks), dim3(256), 0, st,
+                        1, (const float*)l.part, l.T, (int)l.N, a.splits, (__nv_bfloat16*)l.y,
+                        l.ld_y);
+}
+
+}  // namespace moe

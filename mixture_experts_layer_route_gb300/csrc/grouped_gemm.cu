@@ -97,6 +97,37 @@ bool make_scale_map(CUtensorMap* m, const void* base, uint64_t rows, uint32_t co
   return r == CUDA_SUCCESS;
 }
 
+// E2M1 codes two to a byte; see kernels.h.
+bool make_spread_code_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols,
+                          uint32_t box_rows) {
+  auto enc = encoder();
+  if (!enc || cols % 128 != 0) return false;
+  cuuint64_t dims[2] = {cols, rows};
+  cuuint64_t strides[1] = {cols / 2};
+  cuuint32_t box[2] = {128, box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 2, const_cast<void*>(base), dims,
+                         strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
+// 512-byte scale tiles as rows of 128 words.
+bool make_scale_tile_map(CUtensorMap* m, const void* base, uint64_t tiles, uint32_t box_tiles) {
+  auto enc = encoder();
+  if (!enc) return false;
+  cuuint64_t dims[2] = {128, tiles};
+  cuuint64_t strides[1] = {512};
+  cuuint32_t box[2] = {128, box_tiles};
+  cuuint32_t estr[2] = {1, 1};
+  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(base), dims,
+                         strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 namespace {
 
 constexpr int kMaxExperts = 1024;  // the C ABI's limit on E

@@ -29,6 +29,15 @@ bool make_scale_map(CUtensorMap* m, const void* base, uint64_t rows, uint32_t co
 // 16 rows.
 bool make_b_maps(CUtensorMap* m, const void* base, int dtype, uint64_t rows, uint64_t cols,
                  uint32_t b_rows, uint32_t box1);
+// MXFP4 operands (layouts in mxfp4.cuh). E2M1 codes [rows][cols], two to a
+// byte, cols a multiple of 128: boxes of 128 codes x box_rows rows that the
+// load spreads to one code per byte position (16 codes fill 16 bytes: 8 of
+// data, 8 of padding), 128-byte swizzle. x is in codes, a multiple of 128; the
+// load counts 64 bytes per box row.
+bool make_spread_code_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols,
+                          uint32_t box_rows);
+// 512-byte scale tiles, boxes of box_tiles consecutive ones.
+bool make_scale_tile_map(CUtensorMap* m, const void* base, uint64_t tiles, uint32_t box_tiles);
 // Upper bound of the unit count of one grouped-GEMM launch (token tiles of
 // tile_n rows, routed_blocks / shared_blocks feature blocks per group).
 size_t unit_upper_bound(int T, int k, int E, int tile_n, int routed_blocks, int shared_blocks);
@@ -195,6 +204,76 @@ cudaError_t launch_mx_dec_down_gemm(const GemmProblem& p, const MxWeights& w,
                                     const MxDecTokens& h, const int32_t* offsets,
                                     const int32_t* gather_idx, const float* topk_w, float* Y,
                                     int* status, cudaStream_t st);
+
+// MXFP4 (quantize_mxfp4.cu; layouts in mxfp4.cuh). src [rows][cols] bf16 or
+// fp32 with row stride ld -> codes and scale tiles. src2 non-null: the rows of
+// two matrices of groups of I rows (gate, up) alternate in runs of 64 (rows
+// counts both).
+cudaError_t launch_quantize_mxfp4(int dtype, const void* src, const void* src2, int64_t rows,
+                                  int64_t cols, int64_t ld, int64_t I, uint8_t* q, uint8_t* scales,
+                                  int num_sms, cudaStream_t st);
+cudaError_t launch_dequantize_mxfp4(const uint8_t* q, const uint8_t* scales, int64_t rows,
+                                    int64_t cols, int dtype, void* out, int64_t ld, int num_sms,
+                                    cudaStream_t st);
+// Token tiles of an MXFP4 product (gemm_mxfp4.cu): at most `rows` rows, cut in
+// multiples of `unit`, with `row_atoms` 128-row scale tiles each.
+struct Mx4Tiling {
+  bool pairs;  // CTA pairs (cta_group::2)
+  int rows, unit, row_atoms;
+};
+Mx4Tiling mx4_tiling(int64_t T, int tile);
+// The token operand of the MXFP4 products: x [T][K] bf16 (row stride ld) ->
+// codes and, per token tile, its scale tiles. Routed: rows at their slots'
+// positions (checked: MOE_ERR_DEVICE_CHECK), and in token order into shared_q
+// when given.
+struct MxTokenArgs {
+  const void* x;
+  int64_t ld;
+  int T, K, k, E;
+  Mx4Tiling tiling;
+  int vec;  // set by the launch: rows are 16-byte aligned
+  uint8_t *q, *s;
+  uint8_t *shared_q, *shared_s;
+  const int32_t *slot_pos, *topk_ids, *offsets;
+  int* status;
+};
+cudaError_t launch_quantize_tokens(const MxTokenArgs& args, bool routed, bool e2m1, int num_sms,
+                                   cudaStream_t st);
+
+// MXFP4 products (gemm_mxfp4.cu).
+struct Mx4Weights {
+  const uint8_t *gate_up, *s_gate_up, *down, *s_down;
+  const uint8_t *sh_gate_up, *sh_s_gate_up, *sh_down, *sh_s_down;
+};
+struct Mx4Tokens {
+  const uint8_t *routed, *routed_s;  // rows by position [T*k], scale tiles by group
+  const uint8_t *shared, *shared_s;  // rows by token [T]
+};
+struct Mx4Out {
+  uint8_t *routed, *routed_s, *shared, *shared_s;
+};
+cudaError_t launch_mx4_swiglu_gemm(const GemmProblem& p, const Mx4Weights& w, const Mx4Tokens& x,
+                                   const int32_t* offsets, const Mx4Out& h, int* status,
+                                   cudaStream_t st);
+cudaError_t launch_mx4_down_gemm(const GemmProblem& p, const Mx4Weights& w, const Mx4Tokens& h,
+                                 const int32_t* offsets, const int32_t* gather_idx,
+                                 const float* topk_w, float* Y, int* status, cudaStream_t st);
+// y [T][N] = x W^T. splits > 1: fp32 partial sums [splits][T][N] in part,
+// added in split order.
+int mx4_linear_splits(int T, int64_t N, int64_t K, int num_sms);
+struct Mx4Linear {
+  int T;
+  int64_t N, K;
+  bool e2m1, y_f32;
+  const uint8_t *xq, *xs, *wq, *ws;
+  void* y;
+  int64_t ld_y;
+  float* part;
+  int splits, num_sms;
+  int* status;
+  unsigned long long limit_ns;
+};
+cudaError_t launch_mx4_linear(const Mx4Linear& l, cudaStream_t st);
 
 // Combine (combine.cu): y[t] = sum_j Y[t][j] for j < KP, rank order.
 cudaError_t launch_combine(int dtype, const float* Y, int T, int H, int KP, void* y,

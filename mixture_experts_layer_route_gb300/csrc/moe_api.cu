@@ -8,6 +8,7 @@
 #include "moe_api.h"
 #include "common.cuh"
 #include "kernels.h"
+#include "mxfp4.cuh"
 
 namespace moe {
 namespace {
@@ -44,6 +45,9 @@ struct Layout {
   // codes), and the scale rows of h and h_shared (h, hs hold the codes).
   size_t xs, xgs, hsc, hss;
   bool mx_dec;
+  // MXFP4 layers: token codes in expert order (xg) with their scale tiles (xgs
+  // above), in token order for a shared expert (xq, xs); h and h_shared codes
+  // (h, hs) with their scale tiles (hsc, hss).
   int S;  // router split count
 };
 
@@ -62,12 +66,29 @@ bool needs_copy(const moe_problem& p) {
 // Bytes of one element of the expert GEMM operands (E4M3 codes: 1).
 // MXFP8 layers: 2 (their token operands are bf16 rows holding MXFP8 values).
 size_t elem_bytes(int dtype) {
+  if (dtype == MOE_DTYPE_MXFP4) return 1;  // E4M3 activation codes
   return (dtype == MOE_DTYPE_BF16 || dtype == MOE_DTYPE_MXFP8) ? 2
                                                                : (dtype == MOE_DTYPE_E4M3 ? 1 : 4);
 }
-// Dtype of the activations (x, W_router, h, y): bf16 for E4M3 and MXFP8 layers.
+// Dtype of the activations (x, W_router, h, y): bf16 for the layers with
+// quantized weights.
 int act_dtype(int dtype) {
-  return (dtype == MOE_DTYPE_E4M3 || dtype == MOE_DTYPE_MXFP8) ? MOE_DTYPE_BF16 : dtype;
+  return (dtype == MOE_DTYPE_E4M3 || dtype == MOE_DTYPE_MXFP8 || dtype == MOE_DTYPE_MXFP4)
+             ? MOE_DTYPE_BF16
+             : dtype;
+}
+
+// Bytes of the scale tiles of an MXFP4 layer's routed (by expert) or shared (in
+// token order) token rows of `cols` elements.
+size_t mx4_routed_scale_bytes(const moe_problem& p, int64_t cols) {
+  const Mx4Tiling t = mx4_tiling(p.T, p.tile);
+  return (size_t)(group_scale_tile(p.T * p.k, (int)p.E, t.rows) + 1) *
+         (size_t)mxfp4_k_tiles(cols) * (size_t)t.row_atoms * 512;
+}
+size_t mx4_token_scale_bytes(int64_t T, int tile, int64_t cols) {
+  const Mx4Tiling t = mx4_tiling(T, tile);
+  return (size_t)((T + t.rows - 1) / t.rows) * (size_t)mxfp4_k_tiles(cols) *
+         (size_t)t.row_atoms * 512;
 }
 
 // MXFP8 problems with decode-sized token tiles run the E4M3-MMA kernels
@@ -83,7 +104,9 @@ Layout layout_of(const moe_problem& p) {
   const size_t KP = k + (p.I_shared > 0 ? 1 : 0);
   const bool f8 = p.dtype == MOE_DTYPE_E4M3;
   const bool mx = p.dtype == MOE_DTYPE_MXFP8;
-  const size_t as = elem_bytes(act_dtype(p.dtype));
+  const bool m4 = p.dtype == MOE_DTYPE_MXFP4;
+  // Stored h: MXFP4 layers keep it as E4M3 codes.
+  const size_t as = m4 ? 1 : elem_bytes(act_dtype(p.dtype));
   L.S = router_split_count(act_dtype(p.dtype), p.T, p.H, p.E, kRouterSplitSms);
   size_t off = kHeader;
   auto take = [&](size_t bytes) {
@@ -116,10 +139,16 @@ Layout layout_of(const moe_problem& p) {
     L.xgs = take(T * k * skH);
     L.hsc = take(T * k * (size_t)moe_mx_scale_cols(p.I));
     L.hss = p.I_shared > 0 ? take(T * (size_t)moe_mx_scale_cols(p.I_shared)) : 0;
+  } else if (m4) {
+    L.xq = p.I_shared > 0 ? take(T * (size_t)p.H) : 0;
+    L.xs = p.I_shared > 0 ? take(mx4_token_scale_bytes(p.T, p.tile, p.H)) : 0;
+    L.xgs = take(mx4_routed_scale_bytes(p, p.H));
+    L.hsc = take(mx4_routed_scale_bytes(p, p.I));
+    L.hss = p.I_shared > 0 ? take(mx4_token_scale_bytes(p.T, p.tile, p.I_shared)) : 0;
   } else {
     L.xs = L.xgs = L.hsc = L.hss = 0;
   }
-  L.xg = (needs_copy(p) || mx) ? take(T * k * (size_t)p.H * es) : 0;
+  L.xg = (needs_copy(p) || mx || m4) ? take(T * k * (size_t)p.H * es) : 0;
   L.h = take(T * k * (size_t)p.I * as);
   L.hs = p.I_shared > 0 ? take(T * (size_t)p.I_shared * as) : 0;
   L.hq = f8 ? take(T * k * (size_t)p.I) : 0;
@@ -192,10 +221,11 @@ moe_status check_problem(const moe_problem* pb, bool allow_quantized) {
     return MOE_ERR_INVALID_ARG;
   if (p.k > p.E || p.k > 32 || p.E > 1024) return MOE_ERR_INVALID_ARG;
   if (p.H % 128 != 0 || p.I % 64 != 0 || p.I_shared % 64 != 0) return MOE_ERR_INVALID_ARG;
-  const bool quantized = p.dtype == MOE_DTYPE_E4M3 || p.dtype == MOE_DTYPE_MXFP8;
+  const bool quantized = p.dtype == MOE_DTYPE_E4M3 || p.dtype == MOE_DTYPE_MXFP8 ||
+                         p.dtype == MOE_DTYPE_MXFP4;
   if (p.dtype != MOE_DTYPE_BF16 && p.dtype != MOE_DTYPE_F32 && !(allow_quantized && quantized))
     return MOE_ERR_INVALID_ARG;
-  // E4M3 and MXFP8 GEMMs take 128 elements of K per stage.
+  // The quantized GEMMs take 128 elements of K per stage.
   if (quantized && (p.I % 128 != 0 || p.I_shared % 128 != 0)) return MOE_ERR_INVALID_ARG;
   // An MXFP8 weight row's scales (one byte per 32 elements) are loaded as one
   // box of at most 256 bytes.
@@ -268,8 +298,9 @@ moe_status moe_get_workspace_layout(const moe_problem* pb, moe_workspace_layout*
   out->slot_pos = (int64_t)L.slotpos;
   out->h = (int64_t)L.h;
   out->h_shared = pb->I_shared > 0 ? (int64_t)L.hs : -1;
-  out->h_scales = L.mx_dec ? (int64_t)L.hsc : -1;
-  out->h_shared_scales = L.mx_dec && pb->I_shared > 0 ? (int64_t)L.hss : -1;
+  const bool codes = L.mx_dec || pb->dtype == MOE_DTYPE_MXFP4;
+  out->h_scales = codes ? (int64_t)L.hsc : -1;
+  out->h_shared_scales = codes && pb->I_shared > 0 ? (int64_t)L.hss : -1;
   return MOE_OK;
 }
 
@@ -786,6 +817,277 @@ moe_status moe_forward_mx(const moe_problem* pb, const void* x, const void* W_ro
     NvtxRange r("combine");
     e = launch_combine(pb->out_f32 ? MOE_DTYPE_F32 : MOE_DTYPE_BF16, Y, g.T, g.H,
                        g.k + (has_s ? 1 : 0), y, g.num_sms, st);
+  }
+  return cuda_status(e);
+}
+
+moe_status moe_forward_mxfp4(const moe_problem* pb, const void* x, const void* W_router,
+                             const float* router_bias, const uint8_t* Wq_gate_up,
+                             const uint8_t* s_gate_up, const uint8_t* Wq_down,
+                             const uint8_t* s_down, const uint8_t* Wsq_gate_up,
+                             const uint8_t* ss_gate_up, const uint8_t* Wsq_down,
+                             const uint8_t* ss_down, void* y, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  NvtxRange range("moe_forward_mxfp4");
+  if (!pb || pb->dtype != MOE_DTYPE_MXFP4) return MOE_ERR_INVALID_ARG;
+  moe_status s = check_problem(pb, true);
+  if (s != MOE_OK) return s;
+  if (pb->T == 0) return MOE_OK;
+  const bool has_s = pb->I_shared > 0;
+  const void* ptrs[] = {x, W_router, Wq_gate_up, s_gate_up, Wq_down, s_down, y};
+  for (const void* p : ptrs)
+    if (!p || !aligned16(p)) return MOE_ERR_INVALID_ARG;
+  if (router_bias && !aligned16(router_bias)) return MOE_ERR_INVALID_ARG;
+  const void* sptrs[] = {Wsq_gate_up, ss_gate_up, Wsq_down, ss_down};
+  for (const void* p : sptrs) {
+    if (has_s != (p != nullptr)) return MOE_ERR_INVALID_ARG;
+    if (p && !aligned16(p)) return MOE_ERR_INVALID_ARG;
+  }
+  // The weight loads start rows at 32-byte boundaries.
+  const void* codes[] = {Wq_gate_up, Wq_down, Wsq_gate_up, Wsq_down};
+  for (const void* p : codes)
+    if ((reinterpret_cast<uintptr_t>(p) & 31u) != 0) return MOE_ERR_INVALID_ARG;
+  const Layout L = layout_of(*pb);
+  if ((s = check_ws(workspace, workspace_bytes, L.total)) != MOE_OK) return s;
+  if (!tensor_map_encoder_available()) return MOE_ERR_UNSUPPORTED;
+  const GemmProblem g = gemm_problem(*pb);
+
+  cudaStream_t st = (cudaStream_t)stream;
+  int* status = status_ptr(workspace);
+  float* logits = at<float>(workspace, L.logits);
+  float* part = at<float>(workspace, L.partials);
+  int32_t* ids = at<int32_t>(workspace, L.ids);
+  float* w = at<float>(workspace, L.w);
+  int32_t* offs = at<int32_t>(workspace, L.offsets);
+  int32_t* gidx = at<int32_t>(workspace, L.gather);
+  int32_t* spos = at<int32_t>(workspace, L.slotpos);
+  float* Y = at<float>(workspace, L.Y);
+  const Mx4Weights mw = {Wq_gate_up, s_gate_up, Wq_down, s_down,
+                         Wsq_gate_up, ss_gate_up, Wsq_down, ss_down};
+  uint8_t* xq = has_s ? at<uint8_t>(workspace, L.xq) : nullptr;
+  uint8_t* xs = has_s ? at<uint8_t>(workspace, L.xs) : nullptr;
+  const Mx4Tokens xt = {at<uint8_t>(workspace, L.xg), at<uint8_t>(workspace, L.xgs), xq, xs};
+  const Mx4Out ho = {at<uint8_t>(workspace, L.h), at<uint8_t>(workspace, L.hsc),
+                     has_s ? at<uint8_t>(workspace, L.hs) : nullptr,
+                     has_s ? at<uint8_t>(workspace, L.hss) : nullptr};
+  const Mx4Tokens ht = {ho.routed, ho.routed_s, ho.shared, ho.shared_s};
+
+  cudaError_t e = cudaMemsetAsync(status, 0, kHeaderClear, st);
+  // Router, routing and permutation exactly as the bf16 layer (on x itself).
+  if (e == cudaSuccess) {
+    NvtxRange r("router_logits");
+    e = launch_router_logits(MOE_DTYPE_BF16, x, W_router, router_bias, g.T, g.H, g.E, L.S, part,
+                             status, g.limit_ns, st);
+  }
+  if (e == cudaSuccess) {
+    NvtxRange r("route");
+    e = launch_route(part, L.S, router_bias, g.T, g.E, g.k, pb->renorm,
+                     pb->n_group > 1 ? pb->n_group : 1, pb->topk_group,
+                     L.S > 1 ? logits : nullptr, ids, w, st);
+  }
+  if (e == cudaSuccess) {
+    NvtxRange r("permute");
+    e = launch_permute(ids, g.T, g.E, g.k, has_s ? 1 : 0, offs, gidx, spos, status,
+                       at<int32_t>(workspace, L.pscratch), st);
+  }
+  // Token rows to MXFP8 codes and scale tiles, written in expert order.
+  if (e == cudaSuccess) {
+    NvtxRange r("quantize_dispatch_x");
+    MxTokenArgs a = {};
+    a.x = x;
+    a.ld = g.H;
+    a.T = g.T;
+    a.K = g.H;
+    a.k = g.k;
+    a.E = g.E;
+    a.tiling = mx4_tiling(g.T, g.tile);
+    a.q = at<uint8_t>(workspace, L.xg);
+    a.s = at<uint8_t>(workspace, L.xgs);
+    a.shared_q = xq;
+    a.shared_s = xs;
+    a.slot_pos = spos;
+    a.topk_ids = ids;
+    a.offsets = offs;
+    a.status = status;
+    e = launch_quantize_tokens(a, true, false, g.num_sms, st);
+  }
+  if (e == cudaSuccess) {
+    NvtxRange r("gate_up_gemm");
+    e = launch_mx4_swiglu_gemm(g, mw, xt, offs, ho, status, st);
+  }
+  if (e == cudaSuccess) {
+    NvtxRange r("down_gemm");
+    e = launch_mx4_down_gemm(g, mw, ht, offs, gidx, w, Y, status, st);
+  }
+  if (e == cudaSuccess) {
+    NvtxRange r("combine");
+    e = launch_combine(pb->out_f32 ? MOE_DTYPE_F32 : MOE_DTYPE_BF16, Y, g.T, g.H,
+                       g.k + (has_s ? 1 : 0), y, g.num_sms, st);
+  }
+  return cuda_status(e);
+}
+
+int64_t moe_mxfp4_code_cols(int64_t cols) { return cols < 0 ? 0 : mxfp4_code_cols_of(cols); }
+
+int64_t moe_mxfp4_scale_bytes(int64_t rows, int64_t cols) {
+  return rows < 0 || cols < 0 ? 0 : mxfp4_scale_bytes_of(rows, cols);
+}
+
+namespace {
+// Extents of an MXFP4 matrix: 32-bit tensor-map coordinates and k tiles.
+bool mxfp4_extents_ok(int64_t rows, int64_t cols) {
+  const int64_t lim = (int64_t)1 << 30;
+  return rows < lim && cols < lim && (rows + 127) / 128 * mxfp4_k_tiles(cols) < lim;
+}
+}  // namespace
+
+moe_status moe_quantize_mxfp4(const void* src, int32_t src_dtype, int64_t rows, int64_t cols,
+                              int64_t ld, uint8_t* q, uint8_t* scales, void* stream) {
+  NvtxRange range("moe_quantize_mxfp4");
+  if (src_dtype != MOE_DTYPE_BF16 && src_dtype != MOE_DTYPE_F32) return MOE_ERR_INVALID_ARG;
+  if (rows < 0 || cols <= 0 || ld < cols) return MOE_ERR_INVALID_ARG;
+  if (!mxfp4_extents_ok(rows, cols) || ld >= ((int64_t)1 << 40)) return MOE_ERR_UNSUPPORTED;
+  if (rows == 0) return MOE_OK;
+  if (!src || !q || !scales) return MOE_ERR_INVALID_ARG;
+  const uintptr_t es = src_dtype == MOE_DTYPE_BF16 ? 2 : 4;
+  if (reinterpret_cast<uintptr_t>(src) % es != 0 || !aligned16(q) || !aligned16(scales))
+    return MOE_ERR_INVALID_ARG;
+  return cuda_status(launch_quantize_mxfp4(src_dtype, src, nullptr, rows, cols, ld, 0, q, scales,
+                                           sm_count(), (cudaStream_t)stream));
+}
+
+moe_status moe_quantize_mxfp4_gate_up(const void* W_gate, const void* W_up, int32_t src_dtype,
+                                      int64_t E, int64_t I, int64_t H, uint8_t* q, uint8_t* scales,
+                                      void* stream) {
+  NvtxRange range("moe_quantize_mxfp4_gate_up");
+  if (src_dtype != MOE_DTYPE_BF16 && src_dtype != MOE_DTYPE_F32) return MOE_ERR_INVALID_ARG;
+  if (E < 0 || I <= 0 || H <= 0 || I % 64 != 0) return MOE_ERR_INVALID_ARG;
+  const int64_t lim = (int64_t)1 << 30;
+  if (E >= lim || I >= lim || E * I >= lim || !mxfp4_extents_ok(2 * E * I, H))
+    return MOE_ERR_UNSUPPORTED;
+  if (E == 0) return MOE_OK;
+  const void* ptrs[] = {W_gate, W_up, q, scales};
+  for (const void* p : ptrs)
+    if (!p || !aligned16(p)) return MOE_ERR_INVALID_ARG;
+  return cuda_status(launch_quantize_mxfp4(src_dtype, W_gate, W_up, 2 * E * I, H, H, I, q, scales,
+                                           sm_count(), (cudaStream_t)stream));
+}
+
+moe_status moe_dequantize_mxfp4(const uint8_t* q, const uint8_t* scales, int64_t rows, int64_t cols,
+                                void* out, int32_t out_dtype, int64_t ld, void* stream) {
+  NvtxRange range("moe_dequantize_mxfp4");
+  if (out_dtype != MOE_DTYPE_BF16 && out_dtype != MOE_DTYPE_F32) return MOE_ERR_INVALID_ARG;
+  if (rows < 0 || cols <= 0 || ld < cols) return MOE_ERR_INVALID_ARG;
+  if (!mxfp4_extents_ok(rows, cols) || ld >= ((int64_t)1 << 40)) return MOE_ERR_UNSUPPORTED;
+  if (rows == 0) return MOE_OK;
+  if (!out || !q || !scales) return MOE_ERR_INVALID_ARG;
+  const uintptr_t es = out_dtype == MOE_DTYPE_BF16 ? 2 : 4;
+  if (reinterpret_cast<uintptr_t>(out) % es != 0 || !aligned16(q) || !aligned16(scales))
+    return MOE_ERR_INVALID_ARG;
+  return cuda_status(launch_dequantize_mxfp4(q, scales, rows, cols, out_dtype, out, ld, sm_count(),
+                                             (cudaStream_t)stream));
+}
+
+namespace {
+
+struct LinearLayout {
+  size_t xq, xs, part, total;
+  int splits;
+};
+
+// Workspace of moe_linear_mxfp4: status word, token codes, scale tiles, and
+// the partial sums of a split contraction.
+LinearLayout linear_layout(int64_t T, int64_t N, int64_t K, bool e2m1) {
+  LinearLayout L;
+  size_t off = kHeader;
+  auto take = [&](size_t bytes) {
+    const size_t o = off;
+    off = align_up(off + bytes);
+    return o;
+  };
+  L.xq = take((size_t)T * (size_t)mxfp4_k_tiles(K) * (e2m1 ? 64 : 128));
+  L.xs = take(mx4_token_scale_bytes(T, MOE_TILE_AUTO, K));
+  L.splits = mx4_linear_splits((int)T, N, K, kRouterSplitSms);
+  L.part = L.splits > 1 ? take((size_t)L.splits * (size_t)T * (size_t)N * 4) : 0;
+  L.total = off;
+  return L;
+}
+
+moe_status check_linear(int64_t T, int64_t N, int64_t K, int32_t act_dtype) {
+  if (T < 0 || N <= 0 || K <= 0) return MOE_ERR_INVALID_ARG;
+  if (act_dtype != MOE_DTYPE_MXFP8 && act_dtype != MOE_DTYPE_MXFP4) return MOE_ERR_INVALID_ARG;
+  const int64_t lim = (int64_t)1 << 30;
+  if (T >= lim || !mxfp4_extents_ok(N, K) || !mxfp4_extents_ok(T, K) ||
+      (T + 63) / 64 * ((N + 127) / 128) >= lim)
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+}  // namespace
+
+moe_status moe_linear_mxfp4_workspace_size(int64_t T, int64_t N, int64_t K, int32_t act_dtype,
+                                           size_t* bytes) {
+  moe_status s = check_linear(T, N, K, act_dtype);
+  if (s != MOE_OK) return s;
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  *bytes = linear_layout(T, N, K, act_dtype == MOE_DTYPE_MXFP4).total;
+  return MOE_OK;
+}
+
+moe_status moe_linear_mxfp4(const void* x, int64_t T, int64_t K, int64_t ld_x, int32_t act_dtype,
+                            const uint8_t* Wq, const uint8_t* s_W, int64_t N, void* y,
+                            int32_t y_dtype, int64_t ld_y, void* workspace, size_t workspace_bytes,
+                            void* stream) {
+  NvtxRange range("moe_linear_mxfp4");
+  moe_status s = check_linear(T, N, K, act_dtype);
+  if (s != MOE_OK) return s;
+  if (y_dtype != MOE_DTYPE_BF16 && y_dtype != MOE_DTYPE_F32) return MOE_ERR_INVALID_ARG;
+  if (ld_x < K || ld_y < N) return MOE_ERR_INVALID_ARG;
+  if (ld_x >= ((int64_t)1 << 40) || ld_y >= ((int64_t)1 << 40)) return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (!x || !Wq || !s_W || !y) return MOE_ERR_INVALID_ARG;
+  const uintptr_t ys = y_dtype == MOE_DTYPE_BF16 ? 2 : 4;
+  if (reinterpret_cast<uintptr_t>(x) % 2 != 0 || reinterpret_cast<uintptr_t>(y) % ys != 0 ||
+      (reinterpret_cast<uintptr_t>(Wq) & 31u) != 0 || !aligned16(s_W))
+    return MOE_ERR_INVALID_ARG;
+  const bool e2m1 = act_dtype == MOE_DTYPE_MXFP4;
+  const LinearLayout L = linear_layout(T, N, K, e2m1);
+  if ((s = check_ws(workspace, workspace_bytes, L.total)) != MOE_OK) return s;
+  if (!tensor_map_encoder_available()) return MOE_ERR_UNSUPPORTED;
+  cudaStream_t st = (cudaStream_t)stream;
+  cudaError_t e = cudaMemsetAsync(workspace, 0, sizeof(int), st);
+  if (e == cudaSuccess) {
+    NvtxRange r("quantize_x");
+    MxTokenArgs a = {};
+    a.x = x;
+    a.ld = ld_x;
+    a.T = (int)T;
+    a.K = (int)K;
+    a.tiling = mx4_tiling(T, MOE_TILE_AUTO);
+    a.q = at<uint8_t>(workspace, L.xq);
+    a.s = at<uint8_t>(workspace, L.xs);
+    e = launch_quantize_tokens(a, false, e2m1, sm_count(), st);
+  }
+  if (e == cudaSuccess) {
+    NvtxRange r("product");
+    Mx4Linear l = {};
+    l.T = (int)T;
+    l.N = N;
+    l.K = K;
+    l.e2m1 = e2m1;
+    l.y_f32 = y_dtype == MOE_DTYPE_F32;
+    l.xq = at<uint8_t>(workspace, L.xq);
+    l.xs = at<uint8_t>(workspace, L.xs);
+    l.wq = Wq;
+    l.ws = s_W;
+    l.y = y;
+    l.ld_y = ld_y;
+    l.part = L.splits > 1 ? at<float>(workspace, L.part) : nullptr;
+    l.splits = L.splits;
+    l.num_sms = sm_count();
+    l.status = status_ptr(workspace);
+    l.limit_ns = 1000000000ull;
+    e = launch_mx4_linear(l, st);
   }
   return cuda_status(e);
 }

@@ -1,0 +1,97 @@
+// MXFP4 layout and element helpers shared by the quantization kernels and the
+// block-scaled GEMMs.
+//
+// A matrix [rows][cols] is stored as
+//   codes: mxfp4_code_cols(cols) bytes per row, two E2M1 codes to a byte (the
+//     even element in the low half), zeros past the row's end;
+//   scales: one E8M0 byte per 32 elements of a row, in tiles of 128 rows x 4
+//     blocks. A tile is 512 bytes, row r and block b at byte
+//     16 (r % 32) + 4 (r / 32) + b; tiles are row-major over
+//     ceil(rows / 128) x ceil(cols / 128), zeros outside the matrix. This is
+//     the arrangement that one 32-lane x 128-bit scale copy into tensor memory
+//     (tcgen05.cp) takes as it stands: a tile of the GEMM needs no shuffling.
+// E2M1: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp4.h>
+#include <cuda_fp8.h>
+
+#include <cstdint>
+
+#include "mx.cuh"
+
+namespace moe {
+
+// Tiles of 128 elements along a row: the K step of one scale tile.
+__host__ __device__ constexpr int64_t mxfp4_k_tiles(int64_t cols) { return (cols + 127) / 128; }
+__host__ __device__ constexpr int64_t mxfp4_code_cols_of(int64_t cols) {
+  return 64 * mxfp4_k_tiles(cols);
+}
+__host__ __device__ constexpr int64_t mxfp4_scale_bytes_of(int64_t rows, int64_t cols) {
+  return (rows + 127) / 128 * mxfp4_k_tiles(cols) * 512;
+}
+// Byte offset of row r's four scales (a 32-bit word) inside its 512-byte tile.
+__host__ __device__ constexpr uint32_t mxfp4_scale_word(uint32_t r) {
+  return (r & 31u) * 16u + ((r >> 5) & 3u) * 4u;
+}
+
+// Rows of the token tiles that a group of m rows is cut into, at most bn each:
+// an even cut (rounded up to `unit` rows), because an MMA of fewer than 128
+// columns takes as long as one of 128, so 225 rows are two tiles of 128 and 97
+// rather than 224 and 1. Groups of more than four tiles take full ones (the
+// remainder is then a small share, and the rounding cannot empty the last).
+__host__ __device__ constexpr int token_tile_rows(int m, int bn, int unit) {
+  const int tiles = (m + bn - 1) / bn;
+  if (tiles <= 1 || tiles > 4) return bn;
+  const int even = (m + tiles - 1) / tiles;
+  return (even + unit - 1) / unit * unit;
+}
+
+// First scale tile of a group whose rows start at position `first`: groups of
+// m rows need ceil(m / bn) tiles, and first / bn + g leaves at least that many
+// before the next group's without a prefix sum.
+__host__ __device__ constexpr int64_t group_scale_tile(int64_t first, int g, int bn) {
+  return first / bn + g;
+}
+
+// Scale byte of a block from the bits of its largest magnitude: the biased
+// exponent minus `top` (2 for E2M1, 8 for E4M3, whose largest power of two is
+// then the block maximum's), 0 (2^-127) from below, 255 (NaN) for a block that
+// holds an infinity or a NaN.
+__device__ __forceinline__ uint32_t mx_scale_byte(uint32_t amax_bits, int top) {
+  if (amax_bits >= 0x7F800000u) return 255u;
+  const int e = (int)(amax_bits >> 23) - top;
+  return (uint32_t)(e < 0 ? 0 : e);
+}
+
+// 2^(127 - byte), the exact reciprocal of the scale; 0 for the NaN scale, whose
+// codes are then zeros.
+__device__ __forceinline__ float mx_inv_scale(uint32_t byte) {
+  return byte == 255u ? 0.0f : __uint_as_float((254u - byte) << 23);
+}
+
+// v * inv, with the elements of a NaN block (inv = 0) as zeros.
+__device__ __forceinline__ float mx_scaled(float v, float inv) {
+  return inv == 0.0f ? 0.0f : v * inv;
+}
+
+// Two values -> two E2M1 codes in a byte (nearest even, saturating at 6).
+__device__ __forceinline__ uint32_t e2m1_pair(float lo, float hi) {
+  return (uint32_t)__nv_cvt_float2_to_fp4x2(make_float2(lo, hi), __NV_E2M1, cudaRoundNearest);
+}
+
+// A byte of two E2M1 codes -> their values.
+__device__ __forceinline__ float2 e2m1_values(uint32_t byte) {
+  const __half2_raw hr =
+      __nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)(byte & 0xFFu), __NV_E2M1);
+  return __half22float2(*reinterpret_cast<const __half2*>(&hr));
+}
+
+// The scale 2^(byte - 127) of an E8M0 byte; 255 is NaN.
+__device__ __forceinline__ float mx_scale_or_nan(uint32_t byte) {
+  return byte == 255u ? __uint_as_float(0x7FFFFFFFu) : mx_scale_of(byte);
+}
+
+}  // namespace moe

@@ -1,0 +1,317 @@
+"""The MXFP4 operators on the GPU against float64 (mxfp4_reference).
+
+Bars, derived: codes, scale bytes and read-back values are decided by exact
+power-of-two scaling and one rounding, so they are equal bit for bit. A product
+is a sum of exact fp32 products; per MMA (32 or 64 of K) the tensor core adds to
+the fp32 accumulator with an error of at most 2^-22 of the sum of magnitudes S
+(alignment and accumulation, each below 2^-23 S), so K / 32 of them stay within
+K / 32 * 2^-22 S; splits of K add their partial sums with 2^-24 S each, which
+the same bound covers from two MMAs on. bf16 outputs are the fp32 outputs
+rounded, bit for bit. The layer is held to the layer bound of the other weight
+formats (max|d| <= 2e-2 rms, rel-L2 <= 5e-3, fp32 output): its h is quantized
+from fp32 sums, so a few codes sit on the other side of a rounding boundary."""
+import numpy as np
+import pytest
+import torch
+
+import mixture_experts_layer_route_gb300 as m
+import mxfp4_reference as ref
+from moe_inputs import MoEConfig, generate
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def _np(t):
+    return t.double().cpu().numpy()
+
+
+def _rows(rows, cols, dtype, seed, ld=None):
+    """Rows whose blocks span 2^-60..2^60, with zeros, negative zeros and
+    subnormals, as a slice of a buffer with a row stride of ld."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    buf = torch.randn(rows, ld or cols, device=DEV, generator=g)
+    buf *= torch.exp2(torch.randint(-60, 61, buf.shape, device=DEV, generator=g).float() // 1)
+    v = buf[:, :cols]
+    v[0, :33] = 0.0
+    v[-1, ::2] = -0.0
+    v[rows // 2, :4] = torch.tensor([1e-30, -1e-38, 1.0, -2e-40], device=DEV)[:min(4, cols)]
+    return buf.to(dtype)[:, :cols]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,cols,ld", [(1, 1, 1), (3, 31, 31), (5, 33, 40), (130, 200, 203),
+                                          (257, 128, 136), (64, 4096, 4096), (1, 1111, 1111)])
+def test_quantize_and_read_back(rows, cols, ld, dtype):
+    v = _rows(rows, cols, dtype, seed=rows + cols, ld=ld)
+    q, s = m.quantize_mxfp4_rows(v)
+    codes, scales = ref.quantize(_np(v), ref.E2M1, 2)
+    np.testing.assert_array_equal(q.cpu().numpy(), ref.pack(codes))
+    np.testing.assert_array_equal(s.cpu().numpy(), ref.tile(scales, cols))
+    want = ref.values(codes, scales, ref.E2M1)
+    for odt, gap in ((torch.bfloat16, 0), (torch.float32, 0), (torch.bfloat16, 3)):
+        buf = torch.full((rows, cols + gap), 7.0, dtype=odt, device=DEV)
+        m.dequantize_mxfp4(q, s, buf[:, :cols])
+        np.testing.assert_array_equal(_np(buf[:, :cols]), want)
+        assert (buf[:, cols:] == 7.0).all()  # nothing past the row
+
+
+def test_quantize_non_finite_blocks_and_misaligned_base():
+    v = torch.randn(4, 101, device=DEV)
+    v[0, 5], v[1, 40], v[2, 100] = float("nan"), float("inf"), -float("inf")
+    buf = torch.zeros(4 * 101 + 1, device=DEV)
+    v2 = buf[1:].view(4, 101)  # rows of every alignment
+    v2.copy_(v)
+    q, s = m.quantize_mxfp4_rows(v2)
+    codes, scales = ref.quantize(_np(v), ref.E2M1, 2)
+    np.testing.assert_array_equal(s.cpu().numpy(), ref.tile(scales, 101))
+    got = _np(m.dequantize_mxfp4_rows(q, s, 4, 101, torch.float32))
+    np.testing.assert_array_equal(got, ref.values(codes, scales, ref.E2M1))
+
+
+def test_quantize_offsets_past_32_bits():
+    rows, cols = 70001, 32768  # 2.3e9 elements
+    v = torch.zeros(rows, cols, dtype=torch.bfloat16, device=DEV)
+    v[-3:] = torch.randn(3, cols, device=DEV).to(torch.bfloat16)
+    q, s = m.quantize_mxfp4_rows(v)
+    back = m.dequantize_mxfp4_rows(q, s, rows, cols)
+    np.testing.assert_array_equal(_np(back[-3:]), ref.qdq4(_np(v[-3:])))
+    assert not back[:-3].any()
+
+
+def test_gate_up_rows_alternate():
+    E, I, H = 3, 192, 160
+    g = torch.Generator(device=DEV).manual_seed(1)
+    Wg, Wu = (torch.randn(E, I, H, device=DEV, generator=g).to(torch.bfloat16) for _ in range(2))
+    q = torch.empty(E, 2 * I, m.mxfp4_code_cols(H), dtype=torch.uint8, device=DEV)
+    s = torch.empty(m.mxfp4_scale_bytes(2 * E * I, H), dtype=torch.uint8, device=DEV)
+    m.quantize_mxfp4_gate_up(Wg, Wu, q, s)
+    both = torch.stack([Wg.view(E, I // 64, 64, H), Wu.view(E, I // 64, 64, H)], 2)
+    q2, s2 = m.quantize_mxfp4_rows(both.reshape(2 * E * I, H).contiguous())
+    assert torch.equal(q.view(-1), q2.view(-1)) and torch.equal(s, s2)
+
+
+# ------------------------------------------------------------------ linear
+
+def _linear_case(T, N, K, seed, gap=0):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    x = torch.randn(T, K + gap, device=DEV, generator=g)
+    x *= torch.exp2(torch.randint(-3, 4, (T, K + gap), device=DEV, generator=g).float())
+    W = torch.randn(N, K, device=DEV, generator=g)
+    return x.to(torch.bfloat16)[:, :K], W.to(torch.bfloat16)
+
+
+def _check_linear(x, W, act, lin=None):
+    lin = lin or m.LinearMXFP4(W, act=act)
+    T, K = x.shape
+    y32 = lin(x, out_f32=True)
+    y = lin(x)
+    assert m.get_device_status(lin.workspace(T)) == m.MOE_OK
+    xq = torch.tensor((ref.qdq8 if act == "mxfp8" else ref.qdq4)(_np(x)), device=DEV)
+    wq = torch.tensor(ref.qdq4(_np(W)), device=DEV)
+    want, S = xq @ wq.t(), xq.abs() @ wq.abs().t()
+    err = (y32.double() - want).abs()
+    assert (err <= max(K / 32, 1) * 2.0 ** -22 * S).all(), (err / S.clamp(min=1e-300)).max()
+    assert torch.equal(y.view(torch.int16), y32.to(torch.bfloat16).view(torch.int16))
+    return lin, y
+
+
+LINEAR = [(1, 128, 128), (1, 4096, 4096), (3, 1, 1), (16, 200, 130), (17, 129, 416), (33, 640, 1056),
+          (64, 256, 2048), (65, 384, 160), (200, 131, 640), (333, 1000, 1440), (450, 512, 96),
+          (1000, 260, 288)]
+
+
+@pytest.mark.parametrize("act", ["mxfp8", "mxfp4"])
+@pytest.mark.parametrize("T,N,K", LINEAR)
+def test_linear(T, N, K, act):
+    x, W = _linear_case(T, N, K, seed=T + N + K)
+    lin, y = _check_linear(x, W, act)
+    assert torch.equal(lin(x).view(torch.int16), y.view(torch.int16))  # repeats bit for bit
+
+
+@pytest.mark.parametrize("act", ["mxfp8", "mxfp4"])
+@pytest.mark.parametrize("T", [5, 300])
+def test_linear_strided_x_and_out(T, act):
+    N, K = 190, 352
+    x, W = _linear_case(T, N, K, seed=3, gap=5)
+    lin, y = _check_linear(x, W, act)
+    buf = torch.full((T, N + 7), 3.0, dtype=torch.bfloat16, device=DEV)
+    lin(x, out=buf[:, 2:2 + N])
+    assert torch.equal(buf[:, 2:2 + N], y)
+    assert (buf[:, :2] == 3).all() and (buf[:, 2 + N:] == 3).all()
+
+
+@pytest.mark.parametrize("act", ["mxfp8", "mxfp4"])
+@pytest.mark.parametrize("T", [4, 130])
+def test_linear_non_finite_tokens_and_weights(T, act):
+    x, W = _linear_case(T, 256, 512, seed=9)
+    x[1, 77] = float("inf")
+    x[2, 500] = float("nan")
+    W[3, 40] = float("nan")
+    y = m.LinearMXFP4(W, act=act)(x)
+    bad = torch.zeros_like(y, dtype=torch.bool)
+    bad[1:3] = True
+    bad[:, 3] = True
+    assert torch.equal(y.isnan(), bad)
+    x[1:3], W[3] = 0, 0
+    want = m.LinearMXFP4(W, act=act)(x)
+    assert torch.equal(y[~bad], want[~bad])
+
+
+def test_linear_no_tokens_and_other_stream():
+    x, W = _linear_case(40, 384, 640, seed=4)
+    lin = m.LinearMXFP4(W)
+    assert lin(x[:0]).shape == (0, 384)
+    want = lin(x)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    with torch.cuda.stream(st):
+        a = lin(x)
+    b = lin(x, stream=st)
+    st.synchronize()
+    assert torch.equal(a, want) and torch.equal(b, want)
+
+
+def test_linear_refuses_in_python():
+    W = torch.zeros(64, 96, dtype=torch.bfloat16, device=DEV)
+    lin = m.LinearMXFP4(W)
+    with pytest.raises(ValueError):
+        lin(torch.zeros(4, 96, device=DEV))                      # fp32 x
+    with pytest.raises(ValueError):
+        lin(torch.zeros(4, 64, dtype=torch.bfloat16, device=DEV))  # K
+    with pytest.raises(ValueError):
+        lin(torch.zeros(96, 4, dtype=torch.bfloat16, device=DEV).t())  # rows not contiguous
+    with pytest.raises(ValueError):
+        m.LinearMXFP4(W, act="bf16")
+    with pytest.raises(ValueError):
+        m.LinearMXFP4.from_quantized(lin.q[:-1], lin.s, 64, 96)
+
+
+# ------------------------------------------------------------------ layer
+
+CASES = [
+    MoEConfig("decode", T=64, H=512, E=32, k=8, I=256),
+    MoEConfig("token", T=1, H=256, E=16, k=4, I=128),
+    MoEConfig("token_all", T=1, H=128, E=4, k=4, I=128, renorm=0),
+    MoEConfig("shared_small", T=33, H=384, E=8, k=2, I=128, I_shared=256),
+    MoEConfig("many_experts", T=50, H=256, E=512, k=10, I=128),
+    MoEConfig("chunk_shared", T=600, H=256, E=8, k=2, I=256, I_shared=128),
+    MoEConfig("skewed", T=700, H=384, E=64, k=6, I=128, zipf_s=1.1),
+    MoEConfig("heavy", T=1500, H=256, E=4, k=2, I=384),
+    MoEConfig("one_expert", T=257, H=640, E=1, k=1, I=128),
+]
+
+
+def _layer(cfg, seed=0, **kw):
+    d = generate(cfg, seed=seed, device=DEV)
+    lay = m.MoELayerMXFP4(d["W_router"], d["W_gate"], d["W_up"], d["W_down"], cfg.k,
+                          router_bias=d["router_bias"], Ws_gate=d["Ws_gate"], Ws_up=d["Ws_up"],
+                          Ws_down=d["Ws_down"], renorm=cfg.renorm, **kw)
+    return d, lay
+
+
+def _reference(cfg, d):
+    n = {k: None if v is None else _np(v) for k, v in d.items()}
+    shared = (n["Ws_gate"], n["Ws_up"], n["Ws_down"]) if cfg.I_shared else None
+    return ref.layer(n["x"], n["W_router"], n["W_gate"], n["W_up"], n["W_down"], cfg.k,
+                     n["router_bias"], shared, cfg.renorm)
+
+
+def _close(y, want):
+    d = _np(y) - want
+    rms = np.sqrt(np.mean(want ** 2))
+    assert np.abs(d).max() <= 2e-2 * rms, (np.abs(d).max(), rms)
+    assert np.linalg.norm(d) <= 5e-3 * np.linalg.norm(want)
+
+
+@pytest.mark.parametrize("cfg", CASES, ids=[c.name for c in CASES])
+def test_layer(cfg):
+    d, lay = _layer(cfg)
+    y32 = lay(d["x"], out_f32=True)
+    y = lay(d["x"])
+    ws = lay.workspace(cfg.T)
+    assert m.get_device_status(ws) == m.MOE_OK
+    want, ids = _reference(cfg, d)
+    off = m.workspace_layout(lay.problem(cfg.T))["topk_ids"]
+    got = ws[off:off + cfg.T * cfg.k * 4].view(torch.int32).view(cfg.T, cfg.k)
+    np.testing.assert_array_equal(got.cpu().numpy(), ids)
+    _close(y32, want)
+    assert torch.equal(y.view(torch.int16), y32.to(torch.bfloat16).view(torch.int16))
+    assert torch.equal(lay(d["x"]).view(torch.int16), y.view(torch.int16))
+
+
+@pytest.mark.parametrize("tile", [m.MOE_TILE_DECODE, m.MOE_TILE_MEDIUM, m.MOE_TILE_PREFILL])
+@pytest.mark.parametrize("T", [20, 300])
+def test_layer_tile_choices(T, tile):
+    cfg = MoEConfig("tiles", T=T, H=384, E=6, k=2, I=256, I_shared=128)
+    d, lay = _layer(cfg, seed=5, tile=tile)
+    _close(lay(d["x"], out_f32=True), _reference(cfg, d)[0])
+    assert m.get_device_status(lay.workspace(T)) == m.MOE_OK
+
+
+def test_layer_equals_the_mxfp8_layer_on_the_same_values():
+    """E2M1 values are E4M3 values: the MXFP8 layer of the read-back weights
+    computes the same layer by other kernels."""
+    cfg = MoEConfig("same", T=48, H=256, E=8, k=2, I=256, I_shared=128)
+    d, lay = _layer(cfg, seed=2)
+    back = {n: m.dequantize_mxfp4_rows(*m.quantize_mxfp4_rows(d[n]), d[n].numel() // d[n].shape[-1],
+                                       d[n].shape[-1]).view(d[n].shape)
+            for n in ("W_gate", "W_up", "W_down", "Ws_gate", "Ws_up", "Ws_down")}
+    other = m.MoELayerMX(d["W_router"], back["W_gate"], back["W_up"], back["W_down"], cfg.k,
+                         Ws_gate=back["Ws_gate"], Ws_up=back["Ws_up"], Ws_down=back["Ws_down"])
+    _close(lay(d["x"], out_f32=True), _np(other(d["x"], out_f32=True)))
+
+
+def test_layer_no_tokens_and_stream():
+    cfg = MoEConfig("stream", T=24, H=256, E=8, k=2, I=128)
+    d, lay = _layer(cfg)
+    assert lay(d["x"][:0]).shape == (0, 256)
+    want = lay(d["x"])
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    got = lay(d["x"], stream=st)
+    st.synchronize()
+    assert torch.equal(got, want)
+
+
+def test_layer_non_finite_token_stays_in_its_row():
+    cfg = MoEConfig("nan", T=40, H=256, E=8, k=2, I=128)
+    d, lay = _layer(cfg)
+    want = lay(d["x"])
+    x = d["x"].clone()
+    x[7, 100] = float("inf")
+    y = lay(x)
+    torch.cuda.synchronize()
+    keep = torch.arange(40, device=DEV) != 7
+    assert y[7].isnan().all() and torch.equal(y[keep], want[keep])
+
+
+@pytest.mark.parametrize("T", [40, 300])
+def test_layer_bounded_wait_reports_timeout_and_context_survives(T):
+    cfg = MoEConfig("timeout", T=T, H=256, E=8, k=2, I=128)
+    d, lay = _layer(cfg, seed=3)
+    ws = lay.workspace(T)
+    before = lay(d["x"]).clone()
+    pb = lay.problem(T, flags=m.MOE_FLAG_TEST_SKIP_SIGNAL, wait_limit_us=20000)
+    y = torch.empty_like(before)
+    m.forward_mxfp4(pb, d["x"], lay.W_router, None, *lay.gate_up, *lay.down, None, None, None,
+                    None, y, ws)
+    torch.cuda.synchronize()
+    assert m.get_device_status(ws) == 5  # MOE_ERR_TIMEOUT
+    assert torch.equal(lay(d["x"]), before)
+
+
+def test_layer_runs_in_a_graph():
+    cfg = MoEConfig("graph", T=16, H=256, E=8, k=2, I=128)
+    d, lay = _layer(cfg)
+    x = d["x"].clone()
+    out = torch.empty(16, 256, dtype=torch.bfloat16, device=DEV)
+    lay(x, out=out)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        lay(x, out=out)
+    x.copy_(d["x"].flip(0))
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, lay(d["x"].flip(0).contiguous()))

@@ -1,0 +1,148 @@
+"""MXFP4 on the host: the float64 reference of the formats against closed forms,
+the storage sizes, and the argument errors that are found before any launch."""
+import ctypes
+
+import numpy as np
+import pytest
+
+import mixture_experts_layer_route_gb300 as m
+import mxfp4_reference as ref
+from mixture_experts_layer_route_gb300 import build as build_mod
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build_mod.build()
+    return m.load_library()
+
+
+# ------------------------------------------------------------------ the reference
+
+def test_code_tables():
+    assert ref.E4M3[-1] == 448 and ref.E4M3[1] == 2.0 ** -9 and len(ref.E4M3) == 127
+    assert ref.E4M3[8] == 2.0 ** -6 and ref.E4M3[0x38] == 1.0
+
+
+def test_e4m3_nearest_matches_torch():
+    import torch
+    v = torch.linspace(0, 448, 20001, dtype=torch.float32)
+    got = ref._nearest(v.double().numpy(), ref.E4M3)
+    np.testing.assert_array_equal(got, v.to(torch.float8_e4m3fn).view(torch.uint8).numpy())
+
+
+@pytest.mark.parametrize("a,code", [
+    (0.25, 0), (0.2501, 1), (0.75, 2), (1.25, 2), (1.75, 4), (2.5, 4), (3.5, 6), (5.0, 6),
+    (5.01, 7), (7.9, 7),
+])
+def test_e2m1_ties_go_to_the_even_code(a, code):
+    assert ref._nearest(np.array([a]), ref.E2M1)[0] == code
+
+
+def test_block_scale_closed_forms():
+    v = np.zeros((6, 32))
+    v[1, 3] = 6.0            # e = 2 - 2 = 0: 6 is a code
+    v[2, :2] = [7.5, -1.0]   # saturates at 6
+    v[3, 5] = 2.0 ** -140    # held at 2^-127
+    v[4, 0] = np.nan
+    v[5, 31] = -np.inf
+    codes, s = ref.quantize(v, ref.E2M1, 2)
+    assert s[:, 0].tolist() == [0, 127, 127, 0, 255, 255]
+    assert codes[1, 3] == 7 and codes[2, 0] == 7 and codes[2, 1] == 10 and codes[3, 5] == 0
+    q = ref.values(codes, s, ref.E2M1)
+    assert np.isnan(q[4]).all() and np.isnan(q[5]).all() and q[2, 1] == -1.0
+
+
+def test_reference_layout():
+    codes = np.arange(5, dtype=np.uint8)[None]
+    assert ref.pack(codes)[0, :4].tolist() == [0x10, 0x32, 0x04, 0] and ref.pack(codes).shape == (1, 64)
+    s = np.zeros((130, 5), np.uint8)
+    s[33, 4], s[129, 1] = 7, 9
+    t = ref.tile(s, 150)
+    assert t[512 + 16 + 4] == 7 and t[1024 + 16 + 1] == 9 and np.count_nonzero(t) == 2
+
+
+# ------------------------------------------------------------------ sizes and refusals
+
+def test_storage_sizes(lib):
+    assert [m.mxfp4_code_cols(c) for c in (1, 128, 129, 4096)] == [64, 64, 128, 2048]
+    assert [m.mxfp4_scale_bytes(r, c) for r, c in ((1, 1), (128, 128), (129, 128), (256, 4096))] == [
+        512, 512, 1024, 2 * 32 * 512]
+
+
+def test_quantize_refusals(lib):
+    q = lib.moe_quantize_mxfp4
+    assert q(0x1000, 1, 4, 64, 63, 0x2000, 0x3000, None) == 1      # stride below the row
+    assert q(0x1000, 4, 4, 64, 64, 0x2000, 0x3000, None) == 1      # not a source dtype
+    assert q(0x1001, 1, 4, 64, 64, 0x2000, 0x3000, None) == 1      # element alignment
+    assert q(0x1000, 1, 4, 64, 64, 0x2008, 0x3000, None) == 1
+    assert q(0x1000, 1, 4, 64, 64, 0x2000, None, None) == 1
+    assert q(0x1000, 1, 4, 0, 64, 0x2000, 0x3000, None) == 1
+    assert q(0x1000, 1, 1 << 30, 64, 64, 0x2000, 0x3000, None) == 2
+    assert q(None, 1, 0, 64, 64, None, None, None) == 0            # no rows: nothing to do
+    g = lib.moe_quantize_mxfp4_gate_up
+    assert g(0x1000, 0x2000, 1, 2, 96, 64, 0x3000, 0x4000, None) == 1   # I not a multiple of 64
+    assert g(0x1000, None, 1, 2, 64, 64, 0x3000, 0x4000, None) == 1
+    assert g(0x1008, 0x2000, 1, 2, 64, 64, 0x3000, 0x4000, None) == 1
+    d = lib.moe_dequantize_mxfp4
+    assert d(0x1000, 0x2000, 4, 64, 0x3000, 3, 64, None) == 1      # not an output dtype
+    assert d(0x1000, 0x2000, 4, 64, 0x3002, 0, 64, None) == 1      # fp32 alignment
+    assert d(0x1000, 0x2000, 4, 64, 0x3000, 0, 60, None) == 1
+
+
+def test_linear_refusals(lib):
+    def call(x=0x1000, T=4, K=64, ld_x=64, act=3, Wq=0x2000, s=0x3000, N=8, y=0x4000, yd=1,
+             ld_y=8, ws=0x5000, nbytes=1 << 30):
+        return lib.moe_linear_mxfp4(x, T, K, ld_x, act, Wq, s, N, y, yd, ld_y, ws, nbytes, None)
+
+    assert call(act=1) == 1 and call(yd=2) == 1 and call(ld_x=63) == 1 and call(ld_y=7) == 1
+    assert call(N=0) == 1 and call(K=0) == 1 and call(T=-1) == 1
+    assert call(x=None) == 1 and call(x=0x1001) == 1 and call(y=0x4001) == 1
+    assert call(Wq=0x2010) == 1 and call(s=0x3008) == 1 and call(Wq=None) == 1
+    assert call(ws=None) == 3 and call(nbytes=256) == 3
+    assert call(T=1 << 30) == 2
+    assert call(T=0, x=None, Wq=None, s=None, y=None, ws=None, nbytes=0) == 0
+    n = ctypes.c_size_t(0)
+    assert lib.moe_linear_mxfp4_workspace_size(4, 8, 64, 3, ctypes.byref(n)) == 0
+    assert n.value >= 256 + 4 * 128 + 512
+    assert lib.moe_linear_mxfp4_workspace_size(4, 8, 64, 3, None) == 1
+
+
+@pytest.mark.parametrize("kw,code", [(dict(I=192), 1), (dict(I_shared=64), 1), (dict(H=200), 1),
+                                     (dict(k=9), 1)])
+def test_layer_problem_refusals(lib, kw, code):
+    base = dict(T=64, H=256, E=8, k=2, I=128, I_shared=0, dtype="mxfp4")
+    base.update(kw)
+    with pytest.raises(m.MoEError) as ei:
+        m.workspace_size(m.make_problem(**base))
+    assert ei.value.code == code
+
+
+def test_layer_pointer_refusals(lib):
+    def call(pb, shared=False, nbytes=1 << 30, codes=0x3000):
+        sh = [0x20000 + 0x1000 * i for i in range(4)] if shared else [None] * 4
+        return lib.moe_forward_mxfp4(ctypes.byref(pb), 0x1000, 0x2000, None, codes, 0x4000, 0x5000,
+                                     0x6000, *sh, 0x40000, 0x50000, nbytes, None)
+
+    pb = m.make_problem(64, 256, 8, 2, 128, dtype="mxfp4")
+    assert call(m.make_problem(64, 256, 8, 2, 128, dtype="mxfp8")) == 1
+    assert call(pb, shared=True) == 1 and call(pb, nbytes=1024) == 3
+    assert call(pb, codes=0x3010) == 1 and call(pb, codes=None) == 1
+    assert call(m.make_problem(64, 256, 8, 2, 128, I_shared=128, dtype="mxfp4")) == 1
+    # the other entry points refuse the MXFP4 dtype
+    assert lib.moe_forward(ctypes.byref(pb), 0x1000, 0x2000, None, 0x3000, 0x4000, 0x5000, None,
+                           None, None, 0x6000, 0x7000, 1 << 30, None) == 1
+    assert call(m.make_problem(0, 256, 8, 2, 128, dtype="mxfp4"), nbytes=0) == 0
+
+
+@pytest.mark.parametrize("shared", [0, 256])
+@pytest.mark.parametrize("T", [1, 64, 65, 1000])
+def test_layer_workspace_regions_are_disjoint(lib, T, shared):
+    pb = m.make_problem(T, 256, 8, 2, 384, shared, dtype="mxfp4")
+    size, lay = m.workspace_size(pb), m.workspace_layout(pb)
+    bytes_of = dict(logits=T * 8 * 4, topk_ids=T * 8, topk_w=T * 8, expert_offsets=40,
+                    gather_idx=T * 8, slot_pos=T * 8, h=T * 2 * 384, h_shared=T * shared,
+                    h_scales=(T * 2 * 384) // 32, h_shared_scales=T * shared // 32)
+    at = sorted((lay[n], lay[n] + b) for n, b in bytes_of.items() if lay[n] >= 0)
+    assert (lay["h_shared"] >= 0) == (lay["h_shared_scales"] >= 0) == bool(shared)
+    assert all(a >= 256 and a % 256 == 0 and b <= size for a, b in at)
+    assert all(p[1] <= q[0] for p, q in zip(at, at[1:]))
