@@ -21,11 +21,16 @@
 //     from memory fill 16 KB of a stage.
 //   E2M1 tokens (kind::mxf4): both operands packed, two k tiles a stage.
 // Scales travel in groups of KG k tiles through a ring of their own (one box
-// of KG 512-byte tiles for the weights, one of KG x RA for the tokens) and
-// are copied into one of two column ranges of tensor memory by tcgen05.cp. An
-// MMA behind such a copy waits ~200 cycles for it, which is why a group spans
-// several stages: with copies before every stage of four MMAs (63 cycles
-// each, at N <= 128) they took 45% of the tensor pipe's time.
+// of KG 512-byte tiles for the weights, one of KG x RA for the tokens), so that
+// they cost two load instructions a group, and each stage's tiles are copied
+// into one of two column ranges of tensor memory by tcgen05.cp before its MMAs.
+//
+// The producer's and the issuer's loops are run by a whole warp with one
+// elected lane issuing: the operands of TMA and tcgen05 instructions are then
+// provably warp-uniform. A loop under `lane == 0` took 340 cycles for a
+// stage's four MMAs and ~130 for each scale copy; elected, four MMAs with two
+// copies take 212 at N <= 64 (8 KB of weights: 11 TB/s over the chip, above
+// HBM's rate), and the copies hide behind the MMAs.
 //
 // Warp roles: warp 0 TMA producer, warp 1 MMA issuer (one thread) and owner of
 // the tensor memory, the others epilogue (four per group, one 32-lane quarter
@@ -72,7 +77,6 @@ struct Mx4Args {
 template <int MODE, bool F4, int CL, int BN, int STAGES, int KG, int EG>
 struct Mx4Cfg {
   static constexpr int KT_STAGE = F4 ? 2 : 1;          // k tiles per stage
-  static constexpr int SPG = KG / KT_STAGE;            // stages per scale group
   static constexpr int RA = (BN + 127) / 128;          // 128-row scale tiles per token tile
   static constexpr int A_BYTES = 128 * 128;
   static constexpr int A_TX = F4 ? A_BYTES : A_BYTES / 2;  // bytes the load counts
@@ -85,7 +89,8 @@ struct Mx4Cfg {
   static constexpr int SA_BYTES = KG * 512, SB_BYTES = KG * RA * 512;
   static constexpr int SF_BYTES = SA_BYTES + SB_BYTES;
   static constexpr int SF_STAGES = 3;
-  static constexpr int SF_COLS = KG * 4 + KG * RA * 4;
+  // Tensor-memory columns of one stage's scales (two ranges, by stage parity).
+  static constexpr int SF_COLS = KT_STAGE * 4 * (1 + RA);
   static constexpr int USED_COLS = 2 * BN + 2 * SF_COLS;
   static constexpr int TMEM_COLS = USED_COLS <= 256 ? 256 : 512;
   static constexpr int EPI_GROUPS = EG;
@@ -147,6 +152,31 @@ __device__ __forceinline__ void mma_scaled(uint32_t d, uint64_t a, uint64_t b, u
 #undef MOE_MMA_SCALED
 }
 
+// The lane of a converged warp that issues for it.
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}"
+               : "=r"(r));
+  return r != 0;
+}
+
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
+// mbar_wait by a whole warp, with one answer for all of its lanes.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int* status,
+                                          uint64_t limit_ns) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t it = 1;; ++it) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    if ((it & 15u) == 0) {
+      const bool late = globaltimer_ns() - t0 > limit_ns;
+      if (late) set_status(status, MOE_ERR_TIMEOUT);
+      if (__any_sync(0xffffffffu, late || read_status(status) != MOE_OK)) return false;
+    }
+  }
+}
+
 // One unit of work of a CTA (pair): weight row block nb (of 128 rows; pairs
 // take 2 nb and 2 nb + 1) of group g on one token tile, over scale groups
 // [sg0, sg1) of the contraction.
@@ -177,7 +207,7 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, KG, EG>::THRE
   int32_t* offs = prefix + (args.E + 2);
   int32_t* order = offs + (args.E + 2);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   const int E = args.E;
   const int crank = PAIR ? (int)cluster_ctarank() : 0;
   const bool leader = crank == 0;
@@ -283,13 +313,24 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, KG, EG>::THRE
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
+    const bool el = elect_lane();
     const uint64_t pol_w = PAIR ? l2_policy_evict_normal() : l2_policy_evict_first();
     const uint64_t pol_t = l2_policy_evict_last();
+    // A pair's loads all count on the leader's barriers.
+    const uint32_t lead_bars = PAIR ? mapa_shared(bars_base, 0) : bars_base;
+    auto load = [&](uint32_t dst, const CUtensorMap* m, int x, int y, int b, uint64_t pol) {
+      if constexpr (PAIR)
+        tma_load_2d_pair(dst, m, x, y, lead_bars + 8u * (uint32_t)b, pol);
+      else
+        tma_load_2d(dst, m, x, y, bar(b), pol);
+    };
     // Test hook: the first stage is neither signalled nor loaded, so that the
     // MMA issuer's wait on it runs out.
-    const bool skip_first = (args.flags & MOE_FLAG_TEST_SKIP_SIGNAL) != 0;
-    bool skip = skip_first;
-    uint32_t it = 0, sit = 0;
+    const int skip = (args.flags & MOE_FLAG_TEST_SKIP_SIGNAL) != 0 ? 1 : 0;
+    int first = skip * C::KT_STAGE;
+    int s = skip, ss = 0;         // ring positions
+    uint32_t ph = 1, sph = 1;     // and the parities of their empty barriers
+    uint32_t it = (uint32_t)skip, sit = 0;
     bool ok = true;
     for (int u = cid; u < total && ok; u += ncl) {
       const Mx4Tile t = tile_of(u);
@@ -297,77 +338,48 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, KG, EG>::THRE
       const int kt = args.kt[sh];
       // The last row block of a pair may lie past the group's rows: it loads
       // what is there (another group's rows, or zeros) and stores nothing.
-      const int rt = (sh || !GROUPED ? 0 : t.g * (args.rows[0] / 128)) + t.nb;
-      const int need = mma_cols(t) / CL;
+      const int rt = uniform((sh || !GROUPED ? 0 : t.g * (args.rows[0] / 128)) + t.nb);
+      const int need = uniform(mma_cols(t) / CL);
       const int bsel = need <= C::BOX2 ? 2 : (need <= C::BOX1 ? 1 : 0);
       const int box = bsel == 2 ? C::BOX2 : (bsel == 1 ? C::BOX1 : C::B_ROWS);
       const uint32_t tx = CL * (C::A_TX + box * 128);
-      // Lane 0 loads the weights, lane 1 the tokens.
-      const CUtensorMap* my_map = lane == 0 ? &args.tmA[sh] : &args.tmB[sh][bsel];
-      const int my_row = lane == 0 ? rt * 128 : t.p0 + crank * need;
-      const uint32_t my_off = lane == 0 ? 0u : (uint32_t)C::A_BYTES;
-      const uint64_t my_pol = lane == 0 ? pol_w : pol_t;
-      // Elements (E2M1 spread by the load) or bytes a stage along the row.
-      const CUtensorMap* my_smap = lane == 0 ? &args.tmSA[sh] : &args.tmSB[sh];
-      const int64_t s_row0 = lane == 0 ? (int64_t)rt * kt : t.tb * kt * C::RA;
-      const int s_step = lane == 0 ? 1 : C::RA;
-      const uint32_t s_off = lane == 0 ? 0u : (uint32_t)C::SA_BYTES;
-      for (int sg = t.sg0; sg < t.sg1 && ok; ++sg) {
-        {
-          const int s = (int)(sit % C::SF_STAGES);
-          int wok = 1;
-          if (lane == 0)
-            wok = mbar_wait(sfempty_bar(s), ((sit / C::SF_STAGES) & 1u) ^ 1u, args.status, limit);
-          if (!__shfl_sync(0xffffffffu, wok, 0)) {
-            ok = false;
-            break;
-          }
-          ++sit;
-          const uint32_t dst = sfs_base + (uint32_t)(s * C::SF_BYTES) + s_off;
-          if (leader && lane == 0)
-            mbar_arrive_expect_tx(sffull_bar(s), (uint32_t)(CL * C::SF_BYTES));
-          __syncwarp();
-          if (lane < 2) {
-            const int y = (int)(s_row0 + (int64_t)sg * KG * s_step);
-            if constexpr (PAIR)
-              tma_load_2d_pair(dst, my_smap, 0, y, mapa_shared(sffull_bar(s), 0), my_pol);
-            else
-              tma_load_2d(dst, my_smap, 0, y, sffull_bar(s), my_pol);
-          }
+      const int b_row = uniform(t.p0) + crank * need;
+      const CUtensorMap *mA = &args.tmA[sh], *mB = &args.tmB[sh][bsel];
+      const CUtensorMap *mSA = &args.tmSA[sh], *mSB = &args.tmSB[sh];
+      const int sa_row = rt * kt, sb_row = uniform((int)t.tb) * kt * C::RA;
+      const int sg0 = uniform(t.sg0), sg1 = uniform(t.sg1);
+      for (int sg = sg0; sg < sg1; ++sg) {
+        if (!(ok = warp_wait(sfempty_bar(ss), sph, args.status, limit))) break;
+        if (el) {
+          const uint32_t dst = sfs_base + (uint32_t)(ss * C::SF_BYTES);
+          if (leader) mbar_arrive_expect_tx(sffull_bar(ss), (uint32_t)(CL * C::SF_BYTES));
+          load(dst, mSA, 0, sa_row + sg * KG, 2 * STAGES + ss, pol_w);
+          load(dst + C::SA_BYTES, mSB, 0, sb_row + sg * KG * C::RA, 2 * STAGES + ss, pol_t);
         }
+        ++sit;
+        if (++ss == C::SF_STAGES) ss = 0, sph ^= 1u;
         const int kend = min(kt, (sg + 1) * KG);
-        for (int ks = sg * KG; ks < kend; ks += C::KT_STAGE) {
-          const int s = (int)(it % STAGES);
-          int wok = 1;
-          if (lane == 0)
-            wok = mbar_wait(empty_bar(s), ((it / STAGES) & 1u) ^ 1u, args.status, limit);
-          if (!__shfl_sync(0xffffffffu, wok, 0)) {
-            ok = false;
-            break;
+        for (int ks = sg * KG + first; ks < kend; ks += C::KT_STAGE) {
+          if (!(ok = warp_wait(empty_bar(s), ph, args.status, limit))) break;
+          if (el) {
+            const uint32_t dst = stages_base + (uint32_t)(s * C::STAGE_BYTES);
+            const int x = F4 ? ks * 64 : ks * 128;  // bytes, or codes spread by the load
+            if (leader) mbar_arrive_expect_tx(full_bar(s), tx);
+            load(dst, mA, x, rt * 128, s, pol_w);
+            load(dst + C::A_BYTES, mB, x, b_row, s, pol_t);
           }
           ++it;
-          if (skip) {
-            skip = false;
-            continue;
-          }
-          const uint32_t dst = stages_base + (uint32_t)s * C::STAGE_BYTES + my_off;
-          if (leader && lane == 0) mbar_arrive_expect_tx(full_bar(s), tx);
-          __syncwarp();
-          if (lane < 2) {
-            const int x = F4 ? ks * 64 : ks * 128;
-            if constexpr (PAIR)
-              tma_load_2d_pair(dst, my_map, x, my_row, mapa_shared(full_bar(s), 0), my_pol);
-            else
-              tma_load_2d(dst, my_map, x, my_row, full_bar(s), my_pol);
-          }
+          if (++s == STAGES) s = 0, ph ^= 1u;
         }
+        first = 0;
+        if (!ok) break;
       }
     }
     // Let the last loads land before the CTA (pair) can exit.
-    if (lane == 0 && leader) {
+    if (el && leader) {
       const uint32_t n = it < (uint32_t)STAGES ? it : (uint32_t)STAGES;
       for (uint32_t i = it - n; i < it; ++i) {
-        if (skip_first && i == 0) continue;  // never loaded
+        if (skip && i == 0) continue;  // never loaded
         mbar_wait(full_bar((int)(i % STAGES)), (i / STAGES) & 1u, nullptr, 20000000ull);
       }
       const uint32_t m = sit < (uint32_t)C::SF_STAGES ? sit : (uint32_t)C::SF_STAGES;
@@ -378,74 +390,81 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, KG, EG>::THRE
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0 && leader) {
-      uint32_t it = 0, sit = 0, lt = 0;
+    if (leader) {
+      const bool el = elect_lane();
+      auto commit = [&](uint32_t b) {
+        if constexpr (PAIR)
+          umma_commit_pair_multicast(b, 0x3);
+        else
+          umma_commit(b);
+      };
+      // Operand descriptors differ in their start addresses only.
+      const uint64_t dbase = umma_desc_sw128(stages_base), sbase = scale_tile_desc(sfs_base);
+      int s = 0, ss = 0;
+      uint32_t ph = 0, sph = 0, par = 0, lt = 0;
       bool ok = true;
       for (int u = cid; u < total && ok; u += ncl, ++lt) {
         const Mx4Tile t = tile_of(u);
         const int kt = args.kt[GROUPED && t.g == E ? 1 : 0];
+        const int sg0 = uniform(t.sg0), sg1 = uniform(t.sg1);
         const uint32_t acc = lt & 1u;
-        if (!mbar_wait(tempty_bar(acc), ((lt >> 1) & 1u) ^ 1u, args.status, limit)) break;
+        if (!(ok = warp_wait(tempty_bar(acc), ((lt >> 1) & 1u) ^ 1u, args.status, limit))) break;
         tc_fence_after();
         const uint32_t d = tmem_base + acc * BN;
-        uint32_t idesc[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          idesc[i] = F4 ? idesc_scaled(1, 1, 128 * CL, (uint32_t)mma_cols(t), (i & 1) * 2)
-                        : idesc_scaled(5, 0, 128 * CL, (uint32_t)mma_cols(t), i);
+        const uint32_t idesc = idesc_scaled(F4 ? 1 : 5, F4 ? 1 : 0, 128 * CL,
+                                            (uint32_t)uniform(mma_cols(t)), 0);
         uint32_t accumulate = 0;
-        for (int sg = t.sg0; sg < t.sg1 && ok; ++sg, ++sit) {
-          const int ss = (int)(sit % C::SF_STAGES);
-          if (!mbar_wait(sffull_bar(ss), (sit / C::SF_STAGES) & 1u, args.status, limit)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t sa = sf_cols + (sit & 1u) * C::SF_COLS, sb = sa + KG * 4;
-          const uint32_t src = sfs_base + (uint32_t)(ss * C::SF_BYTES);
+        for (int sg = sg0; sg < sg1; ++sg) {
+          if (!(ok = warp_wait(sffull_bar(ss), sph, args.status, limit))) break;
           const int nk = min(KG, kt - sg * KG);
-          for (int i = 0; i < nk; ++i) copy_scale_tile<CL>(sa + i * 4, scale_tile_desc(src + i * 512));
-          for (int i = 0; i < nk * C::RA; ++i)
-            copy_scale_tile<CL>(sb + i * 4, scale_tile_desc(src + C::SA_BYTES + i * 512));
-          if constexpr (PAIR)
-            umma_commit_pair_multicast(sfempty_bar(ss), 0x3);
-          else
-            umma_commit(sfempty_bar(ss));
-          for (int i0 = 0; i0 < nk; i0 += C::KT_STAGE, ++it) {
-            const int s = (int)(it % STAGES);
-            if (!mbar_wait(full_bar(s), (it / STAGES) & 1u, args.status, limit)) {
-              ok = false;
-              break;
-            }
+          for (int i0 = 0; i0 < nk; i0 += C::KT_STAGE) {
+            if (!(ok = warp_wait(full_bar(s), ph, args.status, limit))) break;
             tc_fence_after();
-            const uint32_t a_addr = stages_base + (uint32_t)s * C::STAGE_BYTES;
-            const uint32_t b_addr = a_addr + C::A_BYTES;
+            if (el) {
+              const uint32_t sa = sf_cols + par * C::SF_COLS, sb = sa + C::KT_STAGE * 4;
+              const uint64_t sd = sbase + (uint32_t)((ss * C::SF_BYTES + i0 * 512) >> 4);
+              const uint64_t sbd =
+                  sbase + (uint32_t)((ss * C::SF_BYTES + C::SA_BYTES + i0 * C::RA * 512) >> 4);
+              const uint64_t ad = dbase + (uint32_t)((s * C::STAGE_BYTES) >> 4);
+              const uint64_t bd = ad + (C::A_BYTES >> 4);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int kti = i0 + (F4 ? i >> 1 : 0);  // this MMA's k tile in the group
-              if (F4 && kti >= nk) break;              // an odd last k tile: half a stage
-              mma_scaled<CL, F4>(d, umma_desc_sw128(a_addr + i * 32),
-                                 umma_desc_sw128(b_addr + i * 32), idesc[i], sa + kti * 4,
-                                 sb + kti * 4 * C::RA, accumulate);
-              accumulate = 1;
+              for (int i = 0; i < C::KT_STAGE; ++i)
+                copy_scale_tile<CL>(sa + i * 4, sd + (uint32_t)(i * 32));
+#pragma unroll
+              for (int i = 0; i < C::KT_STAGE * C::RA; ++i)
+                copy_scale_tile<CL>(sb + i * 4, sbd + (uint32_t)(i * 32));
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int kti = F4 ? i >> 1 : 0;             // this MMA's k tile of the stage
+                const uint32_t sf = F4 ? (i & 1) * 2 : i;    // and its first block in the tile
+                if (!F4 || i < 2 || i0 + 1 < nk)             // an odd last k tile: half a stage
+                  mma_scaled<CL, F4>(d, ad + (uint32_t)(i * 2), bd + (uint32_t)(i * 2),
+                                     idesc | (sf << 4) | (sf << 29), sa + kti * 4,
+                                     sb + kti * 4 * C::RA, i == 0 ? accumulate : 1u);
+              }
+              commit(empty_bar(s));
             }
-            if constexpr (PAIR)
-              umma_commit_pair_multicast(empty_bar(s), 0x3);
-            else
-              umma_commit(empty_bar(s));
+            __syncwarp();
+            accumulate = 1;
+            par ^= 1u;
+            if (++s == STAGES) s = 0, ph ^= 1u;
           }
+          if (!ok) break;
+          if (el) commit(sfempty_bar(ss));
+          __syncwarp();
+          if (++ss == C::SF_STAGES) ss = 0, sph ^= 1u;
         }
         if (!ok) break;
-        if constexpr (PAIR)
-          umma_commit_pair_multicast(tfull_bar(acc), 0x3);
-        else
-          umma_commit(tfull_bar(acc));
+        if (el) commit(tfull_bar(acc));
+        __syncwarp();
       }
-      if constexpr (PAIR)
-        umma_commit_pair(drain_bar);
-      else
-        umma_commit(drain_bar);
-      mbar_wait(drain_bar, 0, nullptr, 20000000ull);
+      if (el) {
+        if constexpr (PAIR)
+          umma_commit_pair(drain_bar);
+        else
+          umma_commit(drain_bar);
+        mbar_wait(drain_bar, 0, nullptr, 20000000ull);
+      }
     }
     __syncwarp();
   } else {
