@@ -684,7 +684,11 @@ __global__ void __launch_bounds__(256) split_sum_kernel(const float* __restrict_
 }
 
 constexpr int kMaxExperts = 1024;  // the C ABI's limit on E
-constexpr int kSmallTile = 64;
+// Token tiles: 64 rows on single CTAs (7 stages of 24 KB), 224 rows on pairs (5
+// or 6 stages of 30 KB; two accumulators of 224 columns and the scales fill
+// tensor memory).
+constexpr int kSmallTile = 64, kPairTile = 224;
+constexpr int kScaleGroup = 4;  // k tiles per scale load (KG)
 
 template <int MODE, bool F4, int CL, int BN, int STAGES, int KG, int EG>
 cudaError_t launch_variant(const Mx4Args& a, int num_sms, size_t units, cudaStream_t st) {
@@ -700,12 +704,12 @@ cudaError_t launch_variant(const Mx4Args& a, int num_sms, size_t units, cudaStre
                         CL, a);
 }
 
-// Decode-sized batches: 64-row token tiles on single CTAs; otherwise 224-row
-// tiles on pairs.
 template <int MODE, bool F4>
-cudaError_t launch_mx4(const Mx4Args& a, bool wide, int num_sms, size_t units, cudaStream_t st) {
-  (void)wide;
-  return launch_variant<MODE, F4, 1, kSmallTile, 7, 4, 1>(a, num_sms, units, st);
+cudaError_t launch_mx4(const Mx4Args& a, bool pairs, int num_sms, size_t units, cudaStream_t st) {
+  if (!pairs)
+    return launch_variant<MODE, F4, 1, kSmallTile, 7, kScaleGroup, 1>(a, num_sms, units, st);
+  return launch_variant<MODE, F4, 2, kPairTile, MODE == kDownMx4 ? 6 : 5, kScaleGroup, 2>(
+      a, num_sms, units, st);
 }
 
 struct TokenMaps {
@@ -715,8 +719,9 @@ struct TokenMaps {
   uint64_t tiles;  // token tiles of the scales
 };
 
-template <bool F4, int CL, int BN, int KG>
-bool make_token_maps(CUtensorMap (&m)[3], CUtensorMap* ms, const TokenMaps& t) {
+template <bool F4, int CL, int BN>
+bool make_token_maps_of(CUtensorMap (&m)[3], CUtensorMap* ms, const TokenMaps& t) {
+  constexpr int KG = kScaleGroup;
   using C = Mx4Cfg<kDownMx4, F4, CL, BN, 4, KG, 1>;
   const uint64_t cols = (uint64_t)t.kt * (F4 ? 64 : 128);
   return make_tma_map(&m[0], t.q, MOE_DTYPE_E4M3, t.rows, cols, C::B_ROWS) &&
@@ -725,20 +730,26 @@ bool make_token_maps(CUtensorMap (&m)[3], CUtensorMap* ms, const TokenMaps& t) {
          make_scale_tile_map(ms, t.s, t.tiles * t.kt * C::RA, KG * C::RA);
 }
 
-template <bool F4, int KG>
+template <bool F4>
+bool make_token_maps(CUtensorMap (&m)[3], CUtensorMap* ms, const TokenMaps& t, bool pairs) {
+  return pairs ? make_token_maps_of<F4, 2, kPairTile>(m, ms, t)
+               : make_token_maps_of<F4, 1, kSmallTile>(m, ms, t);
+}
+
+template <bool F4>
 bool make_weight_maps(CUtensorMap* m, CUtensorMap* ms, const uint8_t* q, const uint8_t* s,
                       uint64_t rows, int kt) {
   const bool ok = F4 ? make_tma_map(m, q, MOE_DTYPE_E4M3, rows, (uint64_t)kt * 64, 128)
                      : make_spread_code_map(m, q, rows, (uint64_t)kt * 128, 128);
-  return ok && make_scale_tile_map(ms, s, (rows + 127) / 128 * kt, KG);
+  return ok && make_scale_tile_map(ms, s, (rows + 127) / 128 * kt, kScaleGroup);
 }
 
 }  // namespace
 
 Mx4Tiling mx4_tiling(int64_t T, int tile) {
-  (void)T;
-  (void)tile;
-  return {false, kSmallTile, 16, 1};
+  const bool pairs = tile == MOE_TILE_MEDIUM || tile == MOE_TILE_PREFILL ||
+                     (tile == MOE_TILE_AUTO && T > kSmallTile);
+  return pairs ? Mx4Tiling{true, kPairTile, 32, 2} : Mx4Tiling{false, kSmallTile, 16, 1};
 }
 
 namespace {
@@ -748,7 +759,6 @@ cudaError_t launch_grouped(const GemmProblem& p, const Mx4Weights& w, const Mx4T
                            const int32_t* offsets, const int32_t* gather_idx, const float* topk_w,
                            const Mx4Out& out, float* Y, int* status, cudaStream_t st) {
   constexpr bool GATED = MODE == kGatedMx4;
-  constexpr int KG = 4;
   const bool has_s = p.Is > 0;
   Mx4Args a;
   memset(&a, 0, sizeof(a));
@@ -757,20 +767,21 @@ cudaError_t launch_grouped(const GemmProblem& p, const Mx4Weights& w, const Mx4T
   a.rows[0] = GATED ? 2 * p.I : p.H;
   a.rows[1] = GATED ? (has_s ? 2 * p.Is : 2 * p.I) : p.H;
   const int P = p.T * p.k;
-  const int bn = mx4_tiling(p.T, p.tile).rows;
+  const Mx4Tiling tl = mx4_tiling(p.T, p.tile);
+  const int bn = tl.rows;
   const TokenMaps rt = {x.routed, x.routed_s, (uint64_t)P, a.kt[0],
                         (uint64_t)group_scale_tile(P, p.E, bn) + 1};
   const TokenMaps sh = {x.shared, x.shared_s, (uint64_t)p.T, a.kt[1],
                         (uint64_t)((p.T + bn - 1) / bn)};
-  bool ok = make_weight_maps<false, KG>(&a.tmA[0], &a.tmSA[0], GATED ? w.gate_up : w.down,
+  bool ok = make_weight_maps<false>(&a.tmA[0], &a.tmSA[0], GATED ? w.gate_up : w.down,
                                         GATED ? w.s_gate_up : w.s_down,
                                         (uint64_t)p.E * a.rows[0], a.kt[0]) &&
-            make_token_maps<false, 1, kSmallTile, KG>(a.tmB[0], &a.tmSB[0], rt);
+            make_token_maps<false>(a.tmB[0], &a.tmSB[0], rt, tl.pairs);
   if (ok && has_s)
-    ok = make_weight_maps<false, KG>(&a.tmA[1], &a.tmSA[1], GATED ? w.sh_gate_up : w.sh_down,
+    ok = make_weight_maps<false>(&a.tmA[1], &a.tmSA[1], GATED ? w.sh_gate_up : w.sh_down,
                                      GATED ? w.sh_s_gate_up : w.sh_s_down, (uint64_t)a.rows[1],
                                      a.kt[1]) &&
-         make_token_maps<false, 1, kSmallTile, KG>(a.tmB[1], &a.tmSB[1], sh);
+         make_token_maps<false>(a.tmB[1], &a.tmSB[1], sh, tl.pairs);
   if (!ok) return cudaErrorInvalidValue;
   if (!has_s) {
     a.tmA[1] = a.tmA[0];
@@ -792,9 +803,10 @@ cudaError_t launch_grouped(const GemmProblem& p, const Mx4Weights& w, const Mx4T
   a.E = p.E;
   a.KP = p.k + (has_s ? 1 : 0);
   a.flags = p.flags;
-  const size_t ub = unit_upper_bound(p.T, p.k, p.E, bn, (a.rows[0] + 127) / 128,
-                                     has_s ? (a.rows[1] + 127) / 128 : 0);
-  return launch_mx4<MODE, false>(a, false, p.num_sms, ub, st);
+  const int ur = tl.pairs ? 256 : 128;  // weight rows of a unit
+  const size_t ub = unit_upper_bound(p.T, p.k, p.E, bn, (a.rows[0] + ur - 1) / ur,
+                                     has_s ? (a.rows[1] + ur - 1) / ur : 0);
+  return launch_mx4<MODE, false>(a, tl.pairs, p.num_sms, ub, st);
 }
 
 }  // namespace
@@ -820,18 +832,18 @@ int mx4_linear_splits(int T, int64_t N, int64_t K, int num_sms) {
 }
 
 cudaError_t launch_mx4_linear(const Mx4Linear& l, cudaStream_t st) {
-  constexpr int KG = 4;
   Mx4Args a;
   memset(&a, 0, sizeof(a));
   a.kt[0] = a.kt[1] = (int)mxfp4_k_tiles(l.K);
   a.rows[0] = a.rows[1] = (int)l.N;
-  const int bn = mx4_tiling(l.T, MOE_TILE_AUTO).rows;
+  const Mx4Tiling tl = mx4_tiling(l.T, MOE_TILE_AUTO);
+  const int bn = tl.rows;
   const TokenMaps tm = {l.xq, l.xs, (uint64_t)l.T, a.kt[0], (uint64_t)((l.T + bn - 1) / bn)};
   const bool ok =
-      l.e2m1 ? make_weight_maps<true, KG>(&a.tmA[0], &a.tmSA[0], l.wq, l.ws, l.N, a.kt[0]) &&
-                   make_token_maps<true, 1, kSmallTile, KG>(a.tmB[0], &a.tmSB[0], tm)
-             : make_weight_maps<false, KG>(&a.tmA[0], &a.tmSA[0], l.wq, l.ws, l.N, a.kt[0]) &&
-                   make_token_maps<false, 1, kSmallTile, KG>(a.tmB[0], &a.tmSB[0], tm);
+      l.e2m1 ? make_weight_maps<true>(&a.tmA[0], &a.tmSA[0], l.wq, l.ws, l.N, a.kt[0]) &&
+                   make_token_maps<true>(a.tmB[0], &a.tmSB[0], tm, tl.pairs)
+             : make_weight_maps<false>(&a.tmA[0], &a.tmSA[0], l.wq, l.ws, l.N, a.kt[0]) &&
+                   make_token_maps<false>(a.tmB[0], &a.tmSB[0], tm, tl.pairs);
   if (!ok) return cudaErrorInvalidValue;
   a.tmA[1] = a.tmA[0];
   a.tmSA[1] = a.tmSA[0];
@@ -841,7 +853,7 @@ cudaError_t launch_mx4_linear(const Mx4Linear& l, cudaStream_t st) {
   a.limit_ns = l.limit_ns;
   a.T = l.T;
   a.splits = l.splits;
-  const int sg = (a.kt[0] + KG - 1) / KG;
+  const int sg = (a.kt[0] + kScaleGroup - 1) / kScaleGroup;
   a.groups_per_split = (sg + l.splits - 1) / l.splits;
   a.splits = (sg + a.groups_per_split - 1) / a.groups_per_split;  // no empty split
   const bool part = a.splits > 1;
@@ -850,9 +862,10 @@ cudaError_t launch_mx4_linear(const Mx4Linear& l, cudaStream_t st) {
   a.out_f32 = part || l.y_f32;
   const int es = a.out_f32 ? 4 : 2;
   a.vec_out = (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0 && a.ld_out * es % 16 == 0;
-  const size_t units = (size_t)((l.N + 127) / 128) * ((l.T + bn - 1) / bn) * a.splits;
-  cudaError_t e = l.e2m1 ? launch_mx4<kLinearMx4, true>(a, false, l.num_sms, units, st)
-                         : launch_mx4<kLinearMx4, false>(a, false, l.num_sms, units, st);
+  const int ur = tl.pairs ? 256 : 128;  // weight rows of a unit
+  const size_t units = (size_t)((l.N + ur - 1) / ur) * ((l.T + bn - 1) / bn) * a.splits;
+  cudaError_t e = l.e2m1 ? launch_mx4<kLinearMx4, true>(a, tl.pairs, l.num_sms, units, st)
+                         : launch_mx4<kLinearMx4, false>(a, tl.pairs, l.num_sms, units, st);
   if (e != cudaSuccess || !part) return e;
   int64_t blocks = ((int64_t)l.T * l.N + 255) / 256;
   if (blocks > 8 * (int64_t)l.num_sms) blocks = 8 * (int64_t)l.num_sms;
