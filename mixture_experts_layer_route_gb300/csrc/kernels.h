@@ -237,7 +237,7 @@ struct MxTokenArgs {
   const int32_t *slot_pos, *topk_ids, *offsets;
   int* status;
 };
-cudaError_t launch_quantize_tokens(const MxTokenArgs& args, bool routed, bool e2m1, int num_sms,
+cudaError_t launch_quantize_tokens(const MxTokenArgs& args, bool routed, bool e2m1,
                                    cudaStream_t st);
 
 // MXFP4 products (gemm_mxfp4.cu).

@@ -909,7 +909,7 @@ moe_status moe_forward_mxfp4(const moe_problem* pb, const void* x, const void* W
     a.topk_ids = ids;
     a.offsets = offs;
     a.status = status;
-    e = launch_quantize_tokens(a, true, false, g.num_sms, st);
+    e = launch_quantize_tokens(a, true, false, st);
   }
   if (e == cudaSuccess) {
     NvtxRange r("gate_up_gemm");
@@ -1066,7 +1066,7 @@ moe_status moe_linear_mxfp4(const void* x, int64_t T, int64_t K, int64_t ld_x, i
     a.tiling = mx4_tiling(T, MOE_TILE_AUTO);
     a.q = at<uint8_t>(workspace, L.xq);
     a.s = at<uint8_t>(workspace, L.xs);
-    e = launch_quantize_tokens(a, false, e2m1, sm_count(), st);
+    e = launch_quantize_tokens(a, false, e2m1, st);
   }
   if (e == cudaSuccess) {
     NvtxRange r("product");

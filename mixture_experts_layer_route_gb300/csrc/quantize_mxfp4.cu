@@ -86,6 +86,10 @@ __device__ __forceinline__ uint2 encode8_e4m3(const float (&v)[8], float inv) {
                                mx_scaled(v[7], inv)));
 }
 
+// Blocks are (x: groups of 8 elements of a row, y: rows), so that no thread
+// divides; a thread walks down its column with kRowsAhead rows' loads in flight.
+constexpr int kRowsAhead = 4;
+
 // src [rows][cols] with row stride ld -> codes and tiled scales. PAIRED: row R
 // of the result comes from two matrices (gate, up) of groups of I rows, whose
 // rows alternate in runs of 64.
@@ -94,32 +98,44 @@ __global__ void __launch_bounds__(256) quantize_mxfp4_kernel(
     const TIn* __restrict__ src, const TIn* __restrict__ src2, int64_t rows, int64_t cols,
     int64_t ld, int64_t I, bool vec, uint8_t* __restrict__ q, uint8_t* __restrict__ scales) {
   pdl_entry();
-  const int lane = threadIdx.x & 31;
+  const int lane = (threadIdx.y * blockDim.x + threadIdx.x) & 31;
   const int64_t kt = mxfp4_k_tiles(cols);
-  const int64_t per_row = kt * 16;
-  const int64_t n = (rows + 127) / 128 * 128 * per_row;  // a multiple of 32
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n;
-       i += (int64_t)gridDim.x * blockDim.x) {
-    const int64_t r = i / per_row;
-    const int64_t c8 = i - r * per_row;
-    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (r < rows) {
-      const TIn* row;
-      if constexpr (PAIRED) {
-        const int64_t e = r / (2 * I), w = r - e * 2 * I;
-        row = (((w >> 6) & 1) ? src2 : src) + (e * I + (w >> 7) * 64 + (w & 63)) * ld;
-      } else {
-        row = src + r * ld;
-      }
-      load8(row, c8 * 8, cols, vec, v);
+  const int64_t c8 = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;  // a warp's 32 are in or
+  const bool in = c8 < kt * 16;                                       // out by halves of 16
+  const int64_t padded = (rows + 127) / 128 * 128;  // rows of the scale tiles
+  const int64_t step = (int64_t)gridDim.y * blockDim.y;
+  auto row_of = [&](int64_t r) {
+    if constexpr (PAIRED) {
+      const int64_t e = r / (2 * I), w = r - e * 2 * I;
+      return (((w >> 6) & 1) ? src2 : src) + (e * I + (w >> 7) * 64 + (w & 63)) * ld;
+    } else {
+      return src + r * ld;
     }
-    const uint32_t byte = mx_scale_byte(block_amax_bits(v), kTop4);
-    const uint32_t word = gather_scale_word(byte, lane);
-    if (r < rows)
-      *reinterpret_cast<uint32_t*>(q + r * (kt * 64) + c8 * 4) = encode8_e2m1(v, mx_inv_scale(byte));
-    if ((lane & 15) == 0)
-      *reinterpret_cast<uint32_t*>(scales + ((r >> 7) * kt + (c8 >> 4)) * 512 +
-                                   mxfp4_scale_word((uint32_t)(r & 127))) = word;
+  };
+  // The loop's trip count is the same for all rows of a warp: the bound below
+  // counts whole blocks of rows.
+  const int64_t r0 = (int64_t)blockIdx.y * blockDim.y + threadIdx.y;
+  for (int64_t rb = (int64_t)blockIdx.y * blockDim.y; rb < padded; rb += kRowsAhead * step) {
+    float v[kRowsAhead][8];
+#pragma unroll
+    for (int j = 0; j < kRowsAhead; ++j) {
+      const int64_t r = r0 + (rb - (int64_t)blockIdx.y * blockDim.y) + j * step;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[j][i] = 0.0f;
+      if (in && r < rows) load8(row_of(r), c8 * 8, cols, vec, v[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < kRowsAhead; ++j) {
+      const int64_t r = r0 + (rb - (int64_t)blockIdx.y * blockDim.y) + j * step;
+      const uint32_t byte = mx_scale_byte(block_amax_bits(v[j]), kTop4);
+      const uint32_t word = gather_scale_word(byte, lane);
+      if (in && r < rows)
+        *reinterpret_cast<uint32_t*>(q + r * (kt * 64) + c8 * 4) =
+            encode8_e2m1(v[j], mx_inv_scale(byte));
+      if (in && r < padded && (lane & 15) == 0)
+        *reinterpret_cast<uint32_t*>(scales + ((r >> 7) * kt + (c8 >> 4)) * 512 +
+                                     mxfp4_scale_word((uint32_t)(r & 127))) = word;
+    }
   }
 }
 
@@ -131,44 +147,55 @@ __global__ void __launch_bounds__(256) dequantize_mxfp4_kernel(const uint8_t* __
                                                                bool vec) {
   pdl_entry();
   const int64_t kt = mxfp4_k_tiles(cols);
-  const int64_t per_row = (cols + 7) / 8;
-  const int64_t n = rows * per_row;
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n;
-       i += (int64_t)gridDim.x * blockDim.x) {
-    const int64_t r = i / per_row;
-    const int64_t c8 = i - r * per_row, c = c8 * 8;
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(q + r * (kt * 64) + c8 * 4);
-    const uint32_t byte = scales[((r >> 7) * kt + (c8 >> 4)) * 512 +
-                                 mxfp4_scale_word((uint32_t)(r & 127)) + ((c8 >> 2) & 3)];
-    const float s = mx_scale_or_nan(byte);
-    float v[8];
+  const int64_t c8 = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, c = c8 * 8;
+  if (c >= cols) return;
+  const int64_t step = (int64_t)gridDim.y * blockDim.y;
+  for (int64_t r0 = (int64_t)blockIdx.y * blockDim.y + threadIdx.y; r0 < rows;
+       r0 += kRowsAhead * step) {
+    uint32_t w[kRowsAhead], byte[kRowsAhead];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 f = e2m1_values(w >> (8 * j));
-      v[2 * j] = f.x * s;  // exact: two significant bits, exponents of bf16 and fp32
-      v[2 * j + 1] = f.y * s;
+    for (int j = 0; j < kRowsAhead; ++j) {
+      const int64_t r = r0 + j * step;
+      if (r >= rows) continue;
+      w[j] = *reinterpret_cast<const uint32_t*>(q + r * (kt * 64) + c8 * 4);
+      byte[j] = scales[((r >> 7) * kt + (c8 >> 4)) * 512 + mxfp4_scale_word((uint32_t)(r & 127)) +
+                       ((c8 >> 2) & 3)];
     }
-    TOut* dst = out + r * ld + c;
-    if constexpr (sizeof(TOut) == 2) {
-      if (vec && c + 8 <= cols) {
-        uint32_t o[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
-          o[j] = *reinterpret_cast<const uint32_t*>(&b);
-        }
-        *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
-      } else {
-        for (int j = 0; j < 8; ++j)
-          if (c + j < cols) dst[j] = __float2bfloat16_rn(v[j]);
+    for (int j = 0; j < kRowsAhead; ++j) {
+      const int64_t r = r0 + j * step;
+      if (r >= rows) continue;
+      const float s = mx_scale_or_nan(byte[j]);
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = e2m1_values(w[j] >> (8 * i));
+        v[2 * i] = f.x * s;  // exact: two significant bits, exponents of bf16 and fp32
+        v[2 * i + 1] = f.y * s;
       }
-    } else {
+      TOut* dst = out + r * ld + c;
       if (vec && c + 8 <= cols) {
-        reinterpret_cast<float4*>(dst)[0] = make_float4(v[0], v[1], v[2], v[3]);
-        reinterpret_cast<float4*>(dst)[1] = make_float4(v[4], v[5], v[6], v[7]);
+        if constexpr (sizeof(TOut) == 2) {
+          uint32_t o[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+            o[i] = *reinterpret_cast<const uint32_t*>(&b);
+          }
+          *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+        } else {
+          reinterpret_cast<float4*>(dst)[0] = make_float4(v[0], v[1], v[2], v[3]);
+          reinterpret_cast<float4*>(dst)[1] = make_float4(v[4], v[5], v[6], v[7]);
+        }
       } else {
-        for (int j = 0; j < 8; ++j)
-          if (c + j < cols) dst[j] = v[j];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (c + i < cols) {
+            if constexpr (sizeof(TOut) == 2)
+              dst[i] = __float2bfloat16_rn(v[i]);
+            else
+              dst[i] = v[i];
+          }
       }
     }
   }
@@ -182,76 +209,96 @@ __global__ void __launch_bounds__(256) dequantize_mxfp4_kernel(const uint8_t* __
 // ROUTED: token t's row is written at the positions slot_pos[t k + r] of its k
 // slots, in the scale tile of that expert (rows of an expert are cut into
 // tiles by token_tile_rows), and once in token order for a shared expert
-// (shared_q). Otherwise at row t. One thread = 8 elements of one token; the
-// element work is done once for all k copies.
+// (shared_q). Otherwise at row t. A block takes 2048 elements of one token (8 a
+// thread); its first threads look the k destinations up once for all of it (a
+// look-up per thread took four times as long as the copies), and the element
+// work is done once for all k copies.
 template <bool ROUTED, bool E2M1>
 __global__ void __launch_bounds__(256) quantize_tokens_kernel(MxTokenArgs a) {
   pdl_entry();
+  struct Dest {
+    int64_t row, tile;  // row < 0: none
+    int j;              // row inside the token tile
+  };
+  __shared__ Dest dest[ROUTED ? 33 : 1];
   const int lane = threadIdx.x & 31;
   const int kt = (int)mxfp4_k_tiles(a.K);
   const int per_row = kt * 16;
-  const int64_t n = ((int64_t)a.T * per_row + 31) / 32 * 32;
+  const int chunks = (per_row + 255) / 256;
+  const int t = (int)(blockIdx.x / (unsigned)chunks);
+  const int c8 = (int)(blockIdx.x - (unsigned)t * chunks) * 256 + (int)threadIdx.x;
   const int code_row = (E2M1 ? 64 : 128) * kt;
-  const int P = a.T * a.k;
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n;
-       i += (int64_t)gridDim.x * blockDim.x) {
-    const int t = (int)(i / per_row);
-    const int c8 = (int)(i - (int64_t)t * per_row);
-    const bool live = t < a.T;
-    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (live)
-      load8(reinterpret_cast<const __nv_bfloat16*>(a.x) + (int64_t)t * a.ld, (int64_t)c8 * 8, a.K,
-            a.vec != 0, v);
-    const uint32_t byte = mx_scale_byte(block_amax_bits(v), E2M1 ? kTop4 : kTop8);
-    const uint32_t word = gather_scale_word(byte, lane);
-    const float inv = mx_inv_scale(byte);
-    uint2 codes;
-    if constexpr (E2M1)
-      codes = make_uint2(encode8_e2m1(v, inv), 0);
-    else
-      codes = encode8_e4m3(v, inv);
-    if (!live) continue;
-    auto put = [&](uint8_t* q, uint8_t* s, int64_t row, int64_t tile, int j) {
-      if constexpr (E2M1)
-        *reinterpret_cast<uint32_t*>(q + row * code_row + c8 * 4) = codes.x;
-      else
-        *reinterpret_cast<uint2*>(q + row * code_row + c8 * 8) = codes;
-      if ((c8 & 15) == 0)
-        *reinterpret_cast<uint32_t*>(s + ((tile * kt + (c8 >> 4)) * a.tiling.row_atoms + (j >> 7)) * 512 +
-                                     mxfp4_scale_word((uint32_t)(j & 127))) = word;
-    };
-    if constexpr (ROUTED) {
-      for (int r = 0; r < a.k; ++r) {
-        const int64_t slot = (int64_t)t * a.k + r;
-        const int p = a.slot_pos[slot], e = a.topk_ids[slot];
-        if ((unsigned)p >= (unsigned)P || (unsigned)e >= (unsigned)a.E) {
-          if (c8 == 0) set_status(a.status, MOE_ERR_DEVICE_CHECK);
-          continue;
-        }
+  if constexpr (ROUTED) {
+    if ((int)threadIdx.x < a.k) {
+      const int64_t slot = (int64_t)t * a.k + threadIdx.x;
+      const int p = a.slot_pos[slot], e = a.topk_ids[slot];
+      Dest d = {-1, 0, 0};
+      if ((unsigned)e < (unsigned)a.E && (unsigned)p < (unsigned)(a.T * a.k)) {
         const int first = a.offsets[e], m = a.offsets[e + 1] - first;
         const int local = p - first;
-        if (local < 0 || local >= m) {
-          if (c8 == 0) set_status(a.status, MOE_ERR_DEVICE_CHECK);
-          continue;
+        if (local >= 0 && local < m) {
+          const int tn = token_tile_rows(m, a.tiling.rows, a.tiling.unit);
+          const int mt = local / tn;
+          d = {p, group_scale_tile(first, e, a.tiling.rows) + mt, local - mt * tn};
         }
-        const int tn = token_tile_rows(m, a.tiling.rows, a.tiling.unit);
-        const int mt = local / tn;
-        put(a.q, a.s, p, group_scale_tile(first, e, a.tiling.rows) + mt, local - mt * tn);
       }
+      if (d.row < 0) set_status(a.status, MOE_ERR_DEVICE_CHECK);
+      dest[threadIdx.x] = d;
     }
-    if (!ROUTED || a.shared_q) {
-      const int tn = token_tile_rows(a.T, a.tiling.rows, a.tiling.unit);
-      const int mt = t / tn;
-      put(ROUTED ? a.shared_q : a.q, ROUTED ? a.shared_s : a.s, t, mt, t - mt * tn);
-    }
+  }
+  if (threadIdx.x == 32) {  // the row in token order
+    const int tn = token_tile_rows(a.T, a.tiling.rows, a.tiling.unit);
+    const int mt = t / tn;
+    dest[ROUTED ? 32 : 0] = {t, mt, t - mt * tn};
+  }
+  const bool in = c8 < per_row;
+  float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  if (in)
+    load8(reinterpret_cast<const __nv_bfloat16*>(a.x) + (int64_t)t * a.ld, (int64_t)c8 * 8, a.K,
+          a.vec != 0, v);
+  const uint32_t byte = mx_scale_byte(block_amax_bits(v), E2M1 ? kTop4 : kTop8);
+  const uint32_t word = gather_scale_word(byte, lane);
+  const float inv = mx_inv_scale(byte);
+  uint2 codes;
+  if constexpr (E2M1)
+    codes = make_uint2(encode8_e2m1(v, inv), 0);
+  else
+    codes = encode8_e4m3(v, inv);
+  __syncthreads();
+  if (!in) return;
+  auto put = [&](uint8_t* q, uint8_t* s, const Dest& d) {
+    if (d.row < 0) return;
+    if constexpr (E2M1)
+      *reinterpret_cast<uint32_t*>(q + d.row * code_row + c8 * 4) = codes.x;
+    else
+      *reinterpret_cast<uint2*>(q + d.row * code_row + c8 * 8) = codes;
+    if ((c8 & 15) == 0)
+      *reinterpret_cast<uint32_t*>(
+          s + ((d.tile * kt + (c8 >> 4)) * a.tiling.row_atoms + (d.j >> 7)) * 512 +
+          mxfp4_scale_word((uint32_t)(d.j & 127))) = word;
+  };
+  if constexpr (ROUTED) {
+    for (int r = 0; r < a.k; ++r) put(a.q, a.s, dest[r]);
+    if (a.shared_q) put(a.shared_q, a.shared_s, dest[32]);
+  } else {
+    put(a.q, a.s, dest[0]);
   }
 }
 
-unsigned grid_for(int64_t n, int num_sms) {
-  int64_t blocks = (n + 255) / 256;
-  const int64_t cap = 32 * (int64_t)num_sms;
-  if (blocks > cap) blocks = cap;
-  return (unsigned)(blocks < 1 ? 1 : blocks);
+// Blocks of 256 threads over (8-element groups of a row, rows): as wide as the
+// row up to 256 groups, enough rows in flight to fill the GPU eight blocks deep.
+struct RowGrid {
+  dim3 grid, block;
+};
+RowGrid row_grid(int64_t groups, int64_t rows, int num_sms) {
+  unsigned bx = 16;
+  while (bx < 256 && bx < groups) bx *= 2;
+  const unsigned by = 256 / bx;
+  const int64_t gx = (groups + bx - 1) / bx;
+  int64_t gy = (rows + by - 1) / by;
+  int64_t cap = (8 * (int64_t)num_sms + gx - 1) / gx;
+  if (gy > cap) gy = cap;
+  return {dim3((unsigned)gx, (unsigned)gy), dim3(bx, by)};
 }
 
 bool vec_ok(const void* p, int64_t ld, int es) {
@@ -263,11 +310,11 @@ bool vec_ok(const void* p, int64_t ld, int es) {
 cudaError_t launch_quantize_mxfp4(int dtype, const void* src, const void* src2, int64_t rows,
                                   int64_t cols, int64_t ld, int64_t I, uint8_t* q, uint8_t* scales,
                                   int num_sms, cudaStream_t st) {
-  const unsigned g = grid_for((rows + 127) / 128 * 128 * mxfp4_k_tiles(cols) * 16, num_sms);
+  const RowGrid g = row_grid(mxfp4_k_tiles(cols) * 16, (rows + 127) / 128 * 128, num_sms);
   auto run = [&](auto kernel, auto tag) {
     using T = decltype(tag);
     const bool vec = vec_ok(src, ld, sizeof(T)) && (!src2 || vec_ok(src2, ld, sizeof(T)));
-    return launch_chained(kernel, dim3(g), dim3(256), 0, st, 1, (const T*)src, (const T*)src2,
+    return launch_chained(kernel, g.grid, g.block, 0, st, 1, (const T*)src, (const T*)src2,
                           rows, cols, ld, I, vec, q, scales);
   };
   if (dtype == MOE_DTYPE_BF16)
@@ -280,24 +327,25 @@ cudaError_t launch_quantize_mxfp4(int dtype, const void* src, const void* src2, 
 cudaError_t launch_dequantize_mxfp4(const uint8_t* q, const uint8_t* scales, int64_t rows,
                                     int64_t cols, int dtype, void* out, int64_t ld, int num_sms,
                                     cudaStream_t st) {
-  const unsigned g = grid_for(rows * ((cols + 7) / 8), num_sms);
+  const RowGrid g = row_grid((cols + 7) / 8, rows, num_sms);
   if (dtype == MOE_DTYPE_BF16)
-    return launch_chained(dequantize_mxfp4_kernel<__nv_bfloat16>, dim3(g), dim3(256), 0, st, 1, q,
+    return launch_chained(dequantize_mxfp4_kernel<__nv_bfloat16>, g.grid, g.block, 0, st, 1, q,
                           scales, rows, cols, (__nv_bfloat16*)out, ld, vec_ok(out, ld, 2));
-  return launch_chained(dequantize_mxfp4_kernel<float>, dim3(g), dim3(256), 0, st, 1, q, scales,
+  return launch_chained(dequantize_mxfp4_kernel<float>, g.grid, g.block, 0, st, 1, q, scales,
                         rows, cols, (float*)out, ld, vec_ok(out, ld, 4));
 }
 
-cudaError_t launch_quantize_tokens(const MxTokenArgs& args, bool routed, bool e2m1, int num_sms,
+cudaError_t launch_quantize_tokens(const MxTokenArgs& args, bool routed, bool e2m1,
                                    cudaStream_t st) {
   MxTokenArgs a = args;
   if (a.T == 0) return cudaSuccess;
   a.vec = vec_ok(a.x, a.ld, 2) ? 1 : 0;
-  const unsigned g = grid_for((int64_t)a.T * mxfp4_k_tiles(a.K) * 16, num_sms);
+  const int64_t blocks = (int64_t)a.T * ((mxfp4_k_tiles(a.K) * 16 + 255) / 256);
+  if (blocks >= ((int64_t)1 << 31)) return cudaErrorInvalidValue;
   auto fn = routed ? quantize_tokens_kernel<true, false>
                    : (e2m1 ? quantize_tokens_kernel<false, true>
                            : quantize_tokens_kernel<false, false>);
-  return launch_chained(fn, dim3(g), dim3(256), 0, st, 1, a);
+  return launch_chained(fn, dim3((unsigned)blocks), dim3(256), 0, st, 1, a);
 }
 
 }  // namespace moe
