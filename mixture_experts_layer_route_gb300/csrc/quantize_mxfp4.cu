@@ -19,150 +19,181 @@ namespace {
 
 constexpr int kTop4 = 2, kTop8 = 8;
 
-__device__ __forceinline__ float to_float(float v) { return v; }
-__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+// Eight consecutive elements of a row as loaded, and what a block needs of them.
+template <typename T>
+struct Raw8;
 
-// Elements c .. c + 7 of a row (zeros from `cols` on); vec: 16-byte loads are
-// aligned.
-__device__ __forceinline__ void load8(const __nv_bfloat16* row, int64_t c, int64_t cols, bool vec,
-                                      float (&v)[8]) {
-  if (vec && c + 8 <= cols) {
-    const uint4 u = *reinterpret_cast<const uint4*>(row + c);
-    const __nv_bfloat162* b = reinterpret_cast<const __nv_bfloat162*>(&u);
+template <>
+struct Raw8<__nv_bfloat16> {
+  uint4 u;
+  __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    u = *reinterpret_cast<const uint4*>(p);
+  }
+  // n elements of a row that 16-byte loads may not take, zeros after them.
+  __device__ __forceinline__ void load_some(const __nv_bfloat16* p, int n) {
+    const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w[i] = (2 * i < n ? (uint32_t)h[2 * i] : 0u) |
+             (2 * i + 1 < n ? (uint32_t)h[2 * i + 1] << 16 : 0u);
+    u = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  // fp32 bits of the largest magnitude of the block that four lanes hold (two
+  // 16-bit maxima per instruction).
+  __device__ __forceinline__ uint32_t block_amax_bits() const {
+    const uint32_t k = 0x7FFF7FFFu;
+    uint32_t m = __vmaxu2(__vmaxu2(u.x & k, u.y & k), __vmaxu2(u.z & k, u.w & k));
+    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    return max(m << 16, m & 0xFFFF0000u);
+  }
+  __device__ __forceinline__ void scaled(float inv, float (&v)[8]) const {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float2 f = __bfloat1622float2(b[i]);
-      v[2 * i] = f.x;
-      v[2 * i + 1] = f.y;
+      v[2 * i] = __uint_as_float(w[i] << 16) * inv;
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u) * inv;
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? to_float(row[c + i]) : 0.0f;
   }
-}
-__device__ __forceinline__ void load8(const float* row, int64_t c, int64_t cols, bool vec,
-                                      float (&v)[8]) {
-  if (vec && c + 8 <= cols) {
-    const float4 a = *reinterpret_cast<const float4*>(row + c);
-    const float4 b = *reinterpret_cast<const float4*>(row + c + 4);
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? row[c + i] : 0.0f;
+};
+
+template <>
+struct Raw8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void zero() { a = b = make_float4(0, 0, 0, 0); }
+  __device__ __forceinline__ void load(const float* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
   }
-}
-
-// Bits of the largest magnitude of the block that four lanes hold 8 elements
-// of each. Unsigned bit patterns order magnitudes with infinities and NaNs on
-// top, which a float maximum would drop.
-__device__ __forceinline__ uint32_t block_amax_bits(const float (&v)[8]) {
-  uint32_t a = 0;
+  __device__ __forceinline__ void load_some(const float* p, int n) {
+    float v[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) a = max(a, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-  a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
-  return max(a, __shfl_xor_sync(0xffffffffu, a, 2));
-}
-
-// The four scale bytes of a 128-element tile of a row, from the 16 lanes that
-// hold it (valid in the first of them).
-__device__ __forceinline__ uint32_t gather_scale_word(uint32_t byte, int lane) {
-  uint32_t w = byte << (8 * ((lane >> 2) & 3));
-  w |= __shfl_xor_sync(0xffffffffu, w, 4);
-  return w | __shfl_xor_sync(0xffffffffu, w, 8);
-}
-
-__device__ __forceinline__ uint32_t encode8_e2m1(const float (&v)[8], float inv) {
-  uint32_t w = 0;
+    for (int i = 0; i < 8; ++i) v[i] = i < n ? p[i] : 0.0f;
+    a = make_float4(v[0], v[1], v[2], v[3]);
+    b = make_float4(v[4], v[5], v[6], v[7]);
+  }
+  // Unsigned bit patterns order magnitudes with infinities and NaNs on top,
+  // which a float maximum would drop.
+  __device__ __forceinline__ uint32_t block_amax_bits() const {
+    const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    w |= e2m1_pair(mx_scaled(v[2 * i], inv), mx_scaled(v[2 * i + 1], inv)) << (8 * i);
-  return w;
+    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    return max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  }
+  __device__ __forceinline__ void scaled(float inv, float (&v)[8]) const {
+    const float w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = w[i] * inv;
+  }
+};
+
+// Codes of eight scaled elements; a NaN block (scale byte 255) has zeros.
+template <typename T>
+__device__ __forceinline__ uint32_t encode8_e2m1(const Raw8<T>& r, uint32_t byte) {
+  float v[8];
+  r.scaled(mx_inv_scale(byte), v);
+  uint32_t w = e2m1_pair(v[0], v[1]) | e2m1_pair(v[2], v[3]) << 8 | e2m1_pair(v[4], v[5]) << 16 |
+               e2m1_pair(v[6], v[7]) << 24;
+  return byte == 255u ? 0u : w;
 }
-__device__ __forceinline__ uint2 encode8_e4m3(const float (&v)[8], float inv) {
-  return make_uint2(mx_encode4(mx_scaled(v[0], inv), mx_scaled(v[1], inv), mx_scaled(v[2], inv),
-                               mx_scaled(v[3], inv)),
-                    mx_encode4(mx_scaled(v[4], inv), mx_scaled(v[5], inv), mx_scaled(v[6], inv),
-                               mx_scaled(v[7], inv)));
+template <typename T>
+__device__ __forceinline__ uint2 encode8_e4m3(const Raw8<T>& r, uint32_t byte) {
+  float v[8];
+  r.scaled(mx_inv_scale(byte), v);
+  const uint2 w = make_uint2(mx_encode4(v[0], v[1], v[2], v[3]), mx_encode4(v[4], v[5], v[6], v[7]));
+  return byte == 255u ? make_uint2(0, 0) : w;
 }
 
 // Blocks are (x: groups of 8 elements of a row, y: rows), so that no thread
-// divides; a thread walks down its column with kRowsAhead rows' loads in flight.
-constexpr int kRowsAhead = 4;
-
+// divides; a thread walks down its column with a few rows' loads in flight.
 // src [rows][cols] with row stride ld -> codes and tiled scales. PAIRED: row R
 // of the result comes from two matrices (gate, up) of groups of I rows, whose
-// rows alternate in runs of 64.
-template <typename TIn, bool PAIRED>
+// rows alternate in runs of 64. VEC: rows are 16-byte aligned and whole groups.
+template <typename TIn, bool PAIRED, bool VEC>
 __global__ void __launch_bounds__(256) quantize_mxfp4_kernel(
     const TIn* __restrict__ src, const TIn* __restrict__ src2, int64_t rows, int64_t cols,
-    int64_t ld, int64_t I, bool vec, uint8_t* __restrict__ q, uint8_t* __restrict__ scales) {
+    int64_t ld, int64_t I, uint8_t* __restrict__ q, uint8_t* __restrict__ scales) {
+  constexpr int AHEAD = sizeof(TIn) == 2 ? 4 : 2;
   pdl_entry();
   const int lane = (threadIdx.y * blockDim.x + threadIdx.x) & 31;
   const int64_t kt = mxfp4_k_tiles(cols);
   const int64_t c8 = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;  // a warp's 32 are in or
   const bool in = c8 < kt * 16;                                       // out by halves of 16
+  const int left = (int)min((int64_t)8, cols - c8 * 8);               // elements of this group
   const int64_t padded = (rows + 127) / 128 * 128;  // rows of the scale tiles
   const int64_t step = (int64_t)gridDim.y * blockDim.y;
-  auto row_of = [&](int64_t r) {
+  auto group_of = [&](int64_t r) {
+    const TIn* p;
     if constexpr (PAIRED) {
       const int64_t e = r / (2 * I), w = r - e * 2 * I;
-      return (((w >> 6) & 1) ? src2 : src) + (e * I + (w >> 7) * 64 + (w & 63)) * ld;
+      p = (((w >> 6) & 1) ? src2 : src) + (e * I + (w >> 7) * 64 + (w & 63)) * ld;
     } else {
-      return src + r * ld;
+      p = src + r * ld;
     }
+    return p + c8 * 8;
   };
-  // The loop's trip count is the same for all rows of a warp: the bound below
-  // counts whole blocks of rows.
-  const int64_t r0 = (int64_t)blockIdx.y * blockDim.y + threadIdx.y;
-  for (int64_t rb = (int64_t)blockIdx.y * blockDim.y; rb < padded; rb += kRowsAhead * step) {
-    float v[kRowsAhead][8];
+  // The trip count is the same for all rows of a warp: it counts blocks of rows.
+  int64_t r0 = (int64_t)blockIdx.y * blockDim.y + threadIdx.y;
+  for (int64_t rb = (int64_t)blockIdx.y * blockDim.y; rb < padded;
+       rb += AHEAD * step, r0 += AHEAD * step) {
+    Raw8<TIn> v[AHEAD];
 #pragma unroll
-    for (int j = 0; j < kRowsAhead; ++j) {
-      const int64_t r = r0 + (rb - (int64_t)blockIdx.y * blockDim.y) + j * step;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[j][i] = 0.0f;
-      if (in && r < rows) load8(row_of(r), c8 * 8, cols, vec, v[j]);
+    for (int j = 0; j < AHEAD; ++j) {
+      const int64_t r = r0 + j * step;
+      v[j].zero();
+      if (in && r < rows && left > 0) {
+        if constexpr (VEC)
+          v[j].load(group_of(r));
+        else
+          v[j].load_some(group_of(r), left);
+      }
     }
 #pragma unroll
-    for (int j = 0; j < kRowsAhead; ++j) {
-      const int64_t r = r0 + (rb - (int64_t)blockIdx.y * blockDim.y) + j * step;
-      const uint32_t byte = mx_scale_byte(block_amax_bits(v[j]), kTop4);
-      const uint32_t word = gather_scale_word(byte, lane);
-      if (in && r < rows)
-        *reinterpret_cast<uint32_t*>(q + r * (kt * 64) + c8 * 4) =
-            encode8_e2m1(v[j], mx_inv_scale(byte));
-      if (in && r < padded && (lane & 15) == 0)
-        *reinterpret_cast<uint32_t*>(scales + ((r >> 7) * kt + (c8 >> 4)) * 512 +
-                                     mxfp4_scale_word((uint32_t)(r & 127))) = word;
+    for (int j = 0; j < AHEAD; ++j) {
+      const int64_t r = r0 + j * step;
+      const uint32_t byte = mx_scale_byte(v[j].block_amax_bits(), kTop4);
+      if (!in) continue;
+      if (r < rows)
+        *reinterpret_cast<uint32_t*>(q + r * (kt * 64) + c8 * 4) = encode8_e2m1(v[j], byte);
+      if (r < padded && (lane & 3) == 0)
+        scales[((r >> 7) * kt + (c8 >> 4)) * 512 + mxfp4_scale_word((uint32_t)(r & 127)) +
+               ((c8 >> 2) & 3)] = (uint8_t)byte;
     }
   }
 }
 
-template <typename TOut>
+// VEC: rows of out are 16-byte aligned and whole groups of 8.
+template <typename TOut, bool VEC>
 __global__ void __launch_bounds__(256) dequantize_mxfp4_kernel(const uint8_t* __restrict__ q,
                                                                const uint8_t* __restrict__ scales,
                                                                int64_t rows, int64_t cols,
-                                                               TOut* __restrict__ out, int64_t ld,
-                                                               bool vec) {
+                                                               TOut* __restrict__ out,
+                                                               int64_t ld) {
+  constexpr int AHEAD = 4;
   pdl_entry();
   const int64_t kt = mxfp4_k_tiles(cols);
   const int64_t c8 = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, c = c8 * 8;
   if (c >= cols) return;
+  const int left = (int)min((int64_t)8, cols - c);
   const int64_t step = (int64_t)gridDim.y * blockDim.y;
   for (int64_t r0 = (int64_t)blockIdx.y * blockDim.y + threadIdx.y; r0 < rows;
-       r0 += kRowsAhead * step) {
-    uint32_t w[kRowsAhead], byte[kRowsAhead];
+       r0 += AHEAD * step) {
+    uint32_t w[AHEAD], byte[AHEAD];
 #pragma unroll
-    for (int j = 0; j < kRowsAhead; ++j) {
+    for (int j = 0; j < AHEAD; ++j) {
       const int64_t r = r0 + j * step;
+      w[j] = byte[j] = 0;
       if (r >= rows) continue;
       w[j] = *reinterpret_cast<const uint32_t*>(q + r * (kt * 64) + c8 * 4);
       byte[j] = scales[((r >> 7) * kt + (c8 >> 4)) * 512 + mxfp4_scale_word((uint32_t)(r & 127)) +
                        ((c8 >> 2) & 3)];
     }
 #pragma unroll
-    for (int j = 0; j < kRowsAhead; ++j) {
+    for (int j = 0; j < AHEAD; ++j) {
       const int64_t r = r0 + j * step;
       if (r >= rows) continue;
       const float s = mx_scale_or_nan(byte[j]);
@@ -174,28 +205,26 @@ __global__ void __launch_bounds__(256) dequantize_mxfp4_kernel(const uint8_t* __
         v[2 * i + 1] = f.y * s;
       }
       TOut* dst = out + r * ld + c;
-      if (vec && c + 8 <= cols) {
-        if constexpr (sizeof(TOut) == 2) {
-          uint32_t o[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-            o[i] = *reinterpret_cast<const uint32_t*>(&b);
-          }
-          *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
-        } else {
-          reinterpret_cast<float4*>(dst)[0] = make_float4(v[0], v[1], v[2], v[3]);
-          reinterpret_cast<float4*>(dst)[1] = make_float4(v[4], v[5], v[6], v[7]);
-        }
-      } else {
+      if constexpr (!VEC) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          if (c + i < cols) {
+          if (i < left) {
             if constexpr (sizeof(TOut) == 2)
               dst[i] = __float2bfloat16_rn(v[i]);
             else
               dst[i] = v[i];
           }
+      } else if constexpr (sizeof(TOut) == 2) {
+        uint32_t o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+          o[i] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+        *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+      } else {
+        reinterpret_cast<float4*>(dst)[0] = make_float4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<float4*>(dst)[1] = make_float4(v[4], v[5], v[6], v[7]);
       }
     }
   }
@@ -252,18 +281,26 @@ __global__ void __launch_bounds__(256) quantize_tokens_kernel(MxTokenArgs a) {
     dest[ROUTED ? 32 : 0] = {t, mt, t - mt * tn};
   }
   const bool in = c8 < per_row;
-  float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  if (in)
-    load8(reinterpret_cast<const __nv_bfloat16*>(a.x) + (int64_t)t * a.ld, (int64_t)c8 * 8, a.K,
-          a.vec != 0, v);
-  const uint32_t byte = mx_scale_byte(block_amax_bits(v), E2M1 ? kTop4 : kTop8);
-  const uint32_t word = gather_scale_word(byte, lane);
-  const float inv = mx_inv_scale(byte);
+  Raw8<__nv_bfloat16> v;
+  v.zero();
+  const int left = min(8, a.K - c8 * 8);  // elements of this group
+  if (in && left > 0) {
+    const __nv_bfloat16* p =
+        reinterpret_cast<const __nv_bfloat16*>(a.x) + (int64_t)t * a.ld + c8 * 8;
+    if (a.vec && left == 8)
+      v.load(p);
+    else
+      v.load_some(p, left);
+  }
+  const uint32_t byte = mx_scale_byte(v.block_amax_bits(), E2M1 ? kTop4 : kTop8);
+  uint32_t word = byte << (8 * ((lane >> 2) & 3));  // the k tile's four scale bytes
+  word |= __shfl_xor_sync(0xffffffffu, word, 4);
+  word |= __shfl_xor_sync(0xffffffffu, word, 8);
   uint2 codes;
   if constexpr (E2M1)
-    codes = make_uint2(encode8_e2m1(v, inv), 0);
+    codes = make_uint2(encode8_e2m1(v, byte), 0);
   else
-    codes = encode8_e4m3(v, inv);
+    codes = encode8_e4m3(v, byte);
   __syncthreads();
   if (!in) return;
   auto put = [&](uint8_t* q, uint8_t* s, const Dest& d) {
@@ -311,28 +348,31 @@ cudaError_t launch_quantize_mxfp4(int dtype, const void* src, const void* src2, 
                                   int64_t cols, int64_t ld, int64_t I, uint8_t* q, uint8_t* scales,
                                   int num_sms, cudaStream_t st) {
   const RowGrid g = row_grid(mxfp4_k_tiles(cols) * 16, (rows + 127) / 128 * 128, num_sms);
-  auto run = [&](auto kernel, auto tag) {
+  auto run = [&](auto tag) {
     using T = decltype(tag);
-    const bool vec = vec_ok(src, ld, sizeof(T)) && (!src2 || vec_ok(src2, ld, sizeof(T)));
-    return launch_chained(kernel, g.grid, g.block, 0, st, 1, (const T*)src, (const T*)src2,
-                          rows, cols, ld, I, vec, q, scales);
+    const bool vec = cols % 8 == 0 && vec_ok(src, ld, sizeof(T)) &&
+                     (!src2 || vec_ok(src2, ld, sizeof(T)));
+    auto fn = src2 ? (vec ? quantize_mxfp4_kernel<T, true, true>
+                          : quantize_mxfp4_kernel<T, true, false>)
+                   : (vec ? quantize_mxfp4_kernel<T, false, true>
+                          : quantize_mxfp4_kernel<T, false, false>);
+    return launch_chained(fn, g.grid, g.block, 0, st, 1, (const T*)src, (const T*)src2, rows, cols,
+                          ld, I, q, scales);
   };
-  if (dtype == MOE_DTYPE_BF16)
-    return src2 ? run(quantize_mxfp4_kernel<__nv_bfloat16, true>, __nv_bfloat16())
-                : run(quantize_mxfp4_kernel<__nv_bfloat16, false>, __nv_bfloat16());
-  return src2 ? run(quantize_mxfp4_kernel<float, true>, float())
-              : run(quantize_mxfp4_kernel<float, false>, float());
+  return dtype == MOE_DTYPE_BF16 ? run(__nv_bfloat16()) : run(float());
 }
 
 cudaError_t launch_dequantize_mxfp4(const uint8_t* q, const uint8_t* scales, int64_t rows,
                                     int64_t cols, int dtype, void* out, int64_t ld, int num_sms,
                                     cudaStream_t st) {
   const RowGrid g = row_grid((cols + 7) / 8, rows, num_sms);
-  if (dtype == MOE_DTYPE_BF16)
-    return launch_chained(dequantize_mxfp4_kernel<__nv_bfloat16>, g.grid, g.block, 0, st, 1, q,
-                          scales, rows, cols, (__nv_bfloat16*)out, ld, vec_ok(out, ld, 2));
-  return launch_chained(dequantize_mxfp4_kernel<float>, g.grid, g.block, 0, st, 1, q, scales,
-                        rows, cols, (float*)out, ld, vec_ok(out, ld, 4));
+  auto run = [&](auto tag) {
+    using T = decltype(tag);
+    const bool vec = cols % 8 == 0 && vec_ok(out, ld, sizeof(T));
+    auto fn = vec ? dequantize_mxfp4_kernel<T, true> : dequantize_mxfp4_kernel<T, false>;
+    return launch_chained(fn, g.grid, g.block, 0, st, 1, q, scales, rows, cols, (T*)out, ld);
+  };
+  return dtype == MOE_DTYPE_BF16 ? run(__nv_bfloat16()) : run(float());
 }
 
 cudaError_t launch_quantize_tokens(const MxTokenArgs& args, bool routed, bool e2m1,
