@@ -398,7 +398,7 @@ moe_status moe_dequantize_mxfp4(const uint8_t* q, const uint8_t* scales, int64_t
  * accumulation, one rounding to y_dtype (bf16 or fp32); y has the row stride
  * ld_y. Any T >= 0, N >= 1, K >= 1; x and y need the alignment of their
  * elements only. The workspace (moe_linear_mxfp4_workspace_size bytes) holds
- * the status word, the quantized x and partial sums. */
+ * the status word (cleared by the call) and the quantized x. */
 moe_status moe_linear_mxfp4_workspace_size(int64_t T, int64_t N, int64_t K, int32_t act_dtype,
                                            size_t* bytes);
 moe_status moe_linear_mxfp4(const void* x, int64_t T, int64_t K, int64_t ld_x, int32_t act_dtype,

@@ -16,7 +16,7 @@ import torch
 from ._binding import (  # noqa: F401
     EXPORTED, MOE_DTYPE_BF16, MOE_DTYPE_E4M3, MOE_DTYPE_F32, MOE_DTYPE_MXFP4, MOE_DTYPE_MXFP8,
     MOE_FLAG_TEST_SKIP_SIGNAL, MOE_OK, MOE_TILE_AUTO, MOE_TILE_DECODE, MOE_TILE_MEDIUM,
-    MOE_TILE_PREFILL, STATUS_NAMES, MoEError, MoEProblem, _check_mxfp4, dequantize_mxfp4,
+    MOE_TILE_PREFILL, STATUS_NAMES, MoEError, MoEProblem, _check_mxfp4, _linear_mxfp4, dequantize_mxfp4,
     down_combine, down_combine_noalloc, forward, forward_fp8, forward_mx, forward_mxfp4,
     forward_single_launch, get_device_status, grouped_swiglu_gemm, linear_mxfp4,
     linear_mxfp4_workspace_size, load_library, make_problem, mx_scale_cols, mxfp4_code_cols,
@@ -175,9 +175,9 @@ def quantize_mxfp4_rows(W: torch.Tensor, stream=None):
     as rows of its last dimension, by moe_quantize_mxfp4 (E2M1 with one
     power-of-two scale per block of 32 elements). A matrix may have any row
     stride; W of more dimensions is contiguous."""
-    cols = W.shape[-1]
+    *lead, cols = W.shape
     rows = W.numel() // cols
-    q = torch.empty(W.shape[:-1] + (mxfp4_code_cols(cols),), dtype=torch.uint8, device=W.device)
+    q = torch.empty((*lead, mxfp4_code_cols(cols)), dtype=torch.uint8, device=W.device)
     s = torch.empty(mxfp4_scale_bytes(rows, cols), dtype=torch.uint8, device=W.device)
     quantize_mxfp4(W if W.dim() == 2 else W.view(rows, cols), q, s, stream)
     return q, s
@@ -230,7 +230,9 @@ class LinearMXFP4:
         T = x.shape[0]
         odt = torch.float32 if out_f32 else torch.bfloat16
         y = out if out is not None else torch.empty((T, self.N), dtype=odt, device=x.device)
-        linear_mxfp4(x, self.act, self.q, self.s, self.N, y, self.workspace(T), stream)
+        ws = self.workspace(T)
+        _linear_mxfp4(x, self.act, self.q.data_ptr(), self.s.data_ptr(), self.N, y,
+                      ws.data_ptr(), ws.numel(), stream)
         return y
 
     __call__ = forward

@@ -64,6 +64,8 @@ _I64 = ctypes.c_int64
 def load_library(path: str | None = None) -> ctypes.CDLL:
     """Load libmoe.so (build it with mixture_experts_layer_route_gb300.build)."""
     global _lib
+    if _lib is not None and path is None:
+        return _lib
     with _lock:
         if _lib is not None and path is None:
             return _lib
@@ -133,8 +135,8 @@ def _ptr(t) -> int | None:
 
 
 def _stream(stream) -> int | None:
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:  # the raw handle: a Stream object costs ~3 us a call
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -270,25 +272,29 @@ def forward_mx(problem, x, W_router, router_bias, Wq_gate, s_gate, Wq_up, s_up, 
 
 def mxfp4_code_cols(cols: int) -> int:
     """Bytes of a row of MXFP4 codes for `cols` elements (moe_mxfp4_code_cols)."""
-    return int(load_library().moe_mxfp4_code_cols(int(cols)))
+    return 64 * -(-cols // 128)
 
 
 def mxfp4_scale_bytes(rows: int, cols: int) -> int:
     """Bytes of the MXFP4 scales of a [rows, cols] matrix (moe_mxfp4_scale_bytes)."""
-    return int(load_library().moe_mxfp4_scale_bytes(int(rows), int(cols)))
+    return 512 * -(-rows // 128) * -(-cols // 128)
 
 
-def _float_dtype(t, name: str) -> int:
-    """MOE_DTYPE of a bf16 or fp32 matrix whose rows are contiguous."""
-    if t.dtype not in (torch.bfloat16, torch.float32):
+_FLOAT_DTYPES = {torch.bfloat16: MOE_DTYPE_BF16, torch.float32: MOE_DTYPE_F32}
+
+
+def _float_rows(t, name: str):
+    """(MOE_DTYPE, row stride) of a bf16 or fp32 matrix with contiguous rows."""
+    dt = _FLOAT_DTYPES.get(t.dtype)
+    if dt is None:
         raise ValueError(f"{name}: bf16 or fp32 expected, got {t.dtype}")
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name}: a matrix with contiguous rows expected")
-    return MOE_DTYPE_BF16 if t.dtype == torch.bfloat16 else MOE_DTYPE_F32
-
-
-def _row_stride(t) -> int:
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    if t.dim() != 2:
+        raise ValueError(f"{name}: a matrix expected, got {tuple(t.shape)}")
+    rows, cols = t.shape
+    ld, inner = t.stride()
+    if cols > 1 and inner != 1:
+        raise ValueError(f"{name}: contiguous rows expected, got strides {(ld, inner)}")
+    return dt, ld if rows > 1 else cols
 
 
 def _check_mxfp4(q, scales, rows: int, cols: int, name: str):
@@ -303,11 +309,11 @@ def quantize_mxfp4(src, q, scales, stream=None):
     """MXFP4 codes q [rows, mxfp4_code_cols(cols)] and tiled scales
     (mxfp4_scale_bytes(rows, cols) bytes) of src [rows, cols] (bf16 or fp32,
     contiguous rows, any row stride), as moe_quantize_mxfp4 defines them."""
-    dt = _float_dtype(src, "src")
+    dt, ld = _float_rows(src, "src")
     rows, cols = src.shape
     _check_mxfp4(q, scales, rows, cols, "q, scales")
     _check("moe_quantize_mxfp4", load_library().moe_quantize_mxfp4(
-        _ptr(src), dt, rows, cols, _row_stride(src), _ptr(q), _ptr(scales), _stream(stream)))
+        src.data_ptr(), dt, rows, cols, ld, q.data_ptr(), scales.data_ptr(), _stream(stream)))
 
 
 def quantize_mxfp4_gate_up(W_gate, W_up, q, scales, stream=None):
@@ -317,7 +323,7 @@ def quantize_mxfp4_gate_up(W_gate, W_up, q, scales, stream=None):
     if W_up.shape != W_gate.shape or W_up.dtype != W_gate.dtype or not (
             W_gate.is_contiguous() and W_up.is_contiguous()):
         raise ValueError("W_gate, W_up: two contiguous tensors of one shape and dtype expected")
-    dt = _float_dtype(W_gate.view(E * I, H), "W_gate")
+    dt, _ = _float_rows(W_gate.view(E * I, H), "W_gate")
     _check_mxfp4(q, scales, 2 * E * I, H, "q, scales")
     _check("moe_quantize_mxfp4_gate_up", load_library().moe_quantize_mxfp4_gate_up(
         _ptr(W_gate), _ptr(W_up), dt, E, I, H, _ptr(q), _ptr(scales), _stream(stream)))
@@ -326,11 +332,11 @@ def quantize_mxfp4_gate_up(W_gate, W_up, q, scales, stream=None):
 def dequantize_mxfp4(q, scales, out, stream=None):
     """out [rows, cols] (bf16 or fp32, any row stride): the values of an MXFP4
     matrix (moe_dequantize_mxfp4)."""
-    dt = _float_dtype(out, "out")
+    dt, ld = _float_rows(out, "out")
     rows, cols = out.shape
     _check_mxfp4(q, scales, rows, cols, "q, scales")
     _check("moe_dequantize_mxfp4", load_library().moe_dequantize_mxfp4(
-        _ptr(q), _ptr(scales), rows, cols, _ptr(out), dt, _row_stride(out), _stream(stream)))
+        q.data_ptr(), scales.data_ptr(), rows, cols, out.data_ptr(), dt, ld, _stream(stream)))
 
 
 def linear_mxfp4_workspace_size(T: int, N: int, K: int, act: int) -> int:
@@ -343,16 +349,23 @@ def linear_mxfp4_workspace_size(T: int, N: int, K: int, act: int) -> int:
 def linear_mxfp4(x, act: int, Wq, s_W, N: int, y, workspace, stream=None):
     """y [T, N] (bf16 or fp32) = x [T, K] (bf16) times MXFP4 weights, x quantized
     to `act` (MOE_DTYPE_MXFP8 or MOE_DTYPE_MXFP4), as moe_linear_mxfp4."""
-    if _float_dtype(x, "x") != MOE_DTYPE_BF16:
+    _check_mxfp4(Wq, s_W, N, x.shape[-1], "Wq, s_W")
+    _linear_mxfp4(x, act, Wq.data_ptr(), s_W.data_ptr(), N, y, workspace.data_ptr(),
+                  workspace.numel() * workspace.element_size(), stream)
+
+
+def _linear_mxfp4(x, act, Wq, s_W, N, y, workspace, workspace_bytes, stream):
+    """linear_mxfp4 with the addresses of checked weights and workspace."""
+    xdt, ld_x = _float_rows(x, "x")
+    if xdt != MOE_DTYPE_BF16:
         raise ValueError("x: bf16 expected")
-    dt = _float_dtype(y, "y")
+    dt, ld_y = _float_rows(y, "y")
     T, K = x.shape
-    if tuple(y.shape) != (T, N):
+    if y.shape != (T, N):
         raise ValueError(f"y: shape {(T, N)} expected, got {tuple(y.shape)}")
-    _check_mxfp4(Wq, s_W, N, K, "Wq, s_W")
     _check("moe_linear_mxfp4", load_library().moe_linear_mxfp4(
-        _ptr(x), T, K, _row_stride(x), act, _ptr(Wq), _ptr(s_W), N, _ptr(y), dt, _row_stride(y),
-        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
+        x.data_ptr(), T, K, ld_x, act, Wq, s_W, N, y.data_ptr(), dt, ld_y, workspace,
+        workspace_bytes, _stream(stream)))
 
 
 def forward_mxfp4(problem, x, W_router, router_bias, Wq_gate_up, s_gate_up, Wq_down, s_down,

@@ -52,13 +52,21 @@ namespace {
 enum Mx4Mode : int { kGatedMx4 = 0, kDownMx4 = 1, kLinearMx4 = 2 };
 
 struct Mx4Args {
-  // [0] routed, [1] shared group. B: boxes of B_ROWS, BOX1 and BOX2 rows.
-  CUtensorMap tmA[2], tmSA[2], tmB[2][3], tmSB[2];
+  // [0] routed, [1] shared group. Pairs: token boxes of B_ROWS, BOX1 and BOX2
+  // rows and maps of the scale tiles; single CTAs: one token box (tmB[.][0]),
+  // and the scale tiles as plain addresses (contiguous copies).
+  CUtensorMap tmA[2], tmB[2][3], tmSA[2], tmSB[2];
+  const uint8_t *sA[2], *sB[2];
+  const uint8_t* codes[2];    // the weights' codes, for L2 prefetches
+  int64_t code_bytes[2];
+  // GATED on single CTAs: the down GEMM's routed weights and their row blocks
+  // per expert, whose first units the CTAs ask L2 for at their end.
+  const uint8_t* next_codes;
+  int next_blocks, next_kt;
   const int32_t* offsets;     // [E+2] (GATED, DOWN)
   const int32_t* gather_idx;  // [T*k] (DOWN)
   const float* topk_w;        // [T*k] (DOWN)
-  // GATED: h codes by position; DOWN: Y fp32 [T][KP][H]; LINEAR: y [T][N], or
-  // fp32 partial sums [splits][T][N].
+  // GATED: h codes by position; DOWN: Y fp32 [T][KP][H]; LINEAR: y [T][N].
   void* out;
   uint8_t* out_s;             // GATED: scale tiles of h
   void* out_shared;           // GATED: shared h codes by token, and their scale tiles
@@ -71,18 +79,17 @@ struct Mx4Args {
   unsigned flags;
   // LINEAR
   int64_t ld_out;
-  int out_f32, splits, groups_per_split, vec_out;
+  int out_f32, vec_out;
 };
 
-template <int MODE, bool F4, int CL, int BN, int STAGES, int KG, int EG>
+template <int MODE, bool F4, int CL, int BN, int STAGES, int KG, int EG, bool SPLIT>
 struct Mx4Cfg {
   static constexpr int KT_STAGE = F4 ? 2 : 1;          // k tiles per stage
   static constexpr int RA = (BN + 127) / 128;          // 128-row scale tiles per token tile
   static constexpr int A_BYTES = 128 * 128;
   static constexpr int A_TX = F4 ? A_BYTES : A_BYTES / 2;  // bytes the load counts
   static constexpr int B_ROWS = BN / CL;
-  static constexpr int BOX1 = B_ROWS > 64 ? 64 : 32;
-  static constexpr int BOX2 = B_ROWS > 64 ? 32 : 16;
+  static constexpr int BOX1 = CL == 2 ? 64 : B_ROWS, BOX2 = CL == 2 ? 32 : B_ROWS;
   static constexpr int N_UNIT = 16 * CL;
   static constexpr int B_BYTES = B_ROWS * 128;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
@@ -99,6 +106,7 @@ struct Mx4Cfg {
   static constexpr int EPI_FLOATS = (MODE == kDownMx4 ? 0 : EG * 128 * 33) + 2 * BN;
   // full, empty [STAGES]; sffull, sfempty [SF_STAGES]; tfull, tempty [2]; drain
   static constexpr int NBARS = 2 * STAGES + 2 * SF_STAGES + 5;
+  static_assert(!SPLIT || (MODE == kLinearMx4 && CL == 1), "clusters over K: dense, single CTAs");
   static_assert(USED_COLS <= 512, "tensor memory");
   static_assert(STAGE_BYTES % 1024 == 0 && KG % KT_STAGE == 0, "stage");
 
@@ -181,15 +189,76 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int* st
 // take 2 nb and 2 nb + 1) of group g on one token tile, over scale groups
 // [sg0, sg1) of the contraction.
 struct Mx4Tile {
-  int g, nb, p0, n_valid, sg0, sg1, split;
+  int g, nb, p0, n_valid, sg0, sg1;
   int64_t tb;  // scale tile of the token tile
 };
 
-template <int MODE, bool F4, int CL, int BN, int STAGES, int KG, int EG>
-__global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, KG, EG>::THREADS, 1)
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint32_t bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1], %2, [%3], %4;" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar), "l"(policy)
+      : "memory");
+}
+
+__device__ __forceinline__ uint32_t cluster_nctarank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+// The epilogue's stores of 8 (or 4) consecutive outputs of a row from column n0.
+template <int W>
+__device__ __forceinline__ void store_outputs(const float (&o)[W], void* out, int64_t at, int n0,
+                                              int N, bool f32, bool vec) {
+  const bool whole = vec && n0 + W <= N;
+  if (f32) {
+    float* dst = reinterpret_cast<float*>(out) + at + n0;
+    if (whole) {
+#pragma unroll
+      for (int i = 0; i < W; i += 4)
+        *reinterpret_cast<float4*>(dst + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; ++i)
+        if (n0 + i < N) dst[i] = o[i];
+    }
+  } else {
+    __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(out) + at + n0;
+    if (whole) {
+      uint32_t w[W / 2];
+#pragma unroll
+      for (int i = 0; i < W / 2; ++i) {
+        const __nv_bfloat162 p = __floats2bfloat162_rn(o[2 * i], o[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&p);
+      }
+      if constexpr (W == 8)
+        *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+      else
+        *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; ++i)
+        if (n0 + i < N) dst[i] = __float2bfloat16_rn(o[i]);
+    }
+  }
+}
+
+template <int MODE, bool F4, int CL, int BN, int STAGES, int KG, int EG, bool SPLIT>
+__global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, KG, EG, SPLIT>::THREADS, 1)
     mx4_gemm_kernel(const __grid_constant__ Mx4Args args) {
   pdl_trigger();
-  using C = Mx4Cfg<MODE, F4, CL, BN, STAGES, KG, EG>;
+  using C = Mx4Cfg<MODE, F4, CL, BN, STAGES, KG, EG, SPLIT>;
   constexpr bool PAIR = CL == 2;
   constexpr bool GROUPED = MODE != kLinearMx4;
   extern __shared__ uint8_t smem_raw[];
@@ -211,7 +280,9 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, KG, EG>::THRE
   const int E = args.E;
   const int crank = PAIR ? (int)cluster_ctarank() : 0;
   const bool leader = crank == 0;
-  const int cid = blockIdx.x / CL, ncl = gridDim.x / CL;
+  // SPLIT: a cluster's CTAs share one tile, each with its range of K.
+  const int splits = SPLIT ? (int)cluster_nctarank() : 1;
+  const int cid = blockIdx.x / (CL * splits), ncl = gridDim.x / (CL * splits);
   const uint32_t bars_base = smem_u32(bars);
   auto bar = [&](int i) { return bars_base + 8u * (uint32_t)i; };
   auto full_bar = [&](int s) { return bar(s); };
@@ -233,11 +304,15 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, KG, EG>::THRE
     mbar_init(drain_bar, 1);
     fence_mbar_init();
   }
-  if (warp == 0 && lane < 2) {
+  if (warp == 0 && lane < (GROUPED ? 2 : 1)) {
     tma_prefetch_desc(&args.tmA[lane]);
-    tma_prefetch_desc(&args.tmSA[lane]);
-    tma_prefetch_desc(&args.tmSB[lane]);
-    for (int i = 0; i < 3; ++i) tma_prefetch_desc(&args.tmB[lane][i]);
+    tma_prefetch_desc(&args.tmB[lane][0]);
+    if constexpr (PAIR) {
+      tma_prefetch_desc(&args.tmSA[lane]);
+      tma_prefetch_desc(&args.tmSB[lane]);
+      tma_prefetch_desc(&args.tmB[lane][1]);
+      tma_prefetch_desc(&args.tmB[lane][2]);
+    }
   }
   if (warp == 1) {
     if constexpr (PAIR)
@@ -270,7 +345,7 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, KG, EG>::THRE
   } else {
     lin_nb = (args.rows[0] + 128 * CL - 1) / (128 * CL);
     lin_mt = (args.T + BN - 1) / BN;
-    total = lin_nb * lin_mt * args.splits;
+    total = lin_nb * lin_mt;
   }
   auto tile_of = [&](int u) {
     Mx4Tile t;
@@ -286,20 +361,19 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, KG, EG>::THRE
       t.p0 = tl.g == E ? 0 : offs[tl.g];  // the shared group's rows are in token order
       t.sg0 = 0;
       t.sg1 = (args.kt[tl.g == E] + KG - 1) / KG;
-      t.split = 0;
     } else {
       // Token tiles fastest, so that the CTAs at work share weight rows in L2.
       t.g = 0;
       mt = u % lin_mt;
       const int v = u / lin_mt;
-      t.nb = (v % lin_nb) * CL + crank;
-      t.split = v / lin_nb;
+      t.nb = v * CL + crank;
       m = args.T;
       t.tb = 0;
       t.p0 = 0;
       const int sg = (args.kt[0] + KG - 1) / KG;
-      t.sg0 = t.split * args.groups_per_split;
-      t.sg1 = min(sg, t.sg0 + args.groups_per_split);
+      const int rank = SPLIT ? (int)cluster_ctarank() : 0;
+      t.sg0 = rank * sg / splits;  // never empty: splits <= sg
+      t.sg1 = (rank + 1) * sg / splits;
     }
     const int tn = token_tile_rows(m, BN, C::N_UNIT);
     t.tb += mt;
@@ -324,6 +398,30 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, KG, EG>::THRE
       else
         tma_load_2d(dst, m, x, y, bar(b), pol);
     };
+    // L2 prefetches (single CTAs): a unit's codes are one contiguous range
+    // (128 whole rows). The ring holds 8 KB of codes a stage, too little in
+    // flight to cover HBM's latency; the next unit's codes are therefore asked
+    // of L2 a group's share at a time while this unit's are loaded, and the
+    // first unit's at once. Decode layer T=64: 261 -> 217 us (see the table).
+    constexpr bool PREFETCH = !PAIR && !SPLIT;
+    constexpr uint32_t PF_BYTES = KG * 8192;
+    auto prefetch_codes = [&](int sh, int rt, int part) {
+      const int64_t row_block = (int64_t)args.kt[sh] * 8192;
+      const int64_t at = (int64_t)rt * row_block + (int64_t)part * PF_BYTES;
+      const int64_t end = min((int64_t)(rt + 1) * row_block, args.code_bytes[sh]);
+      if (at < end)
+        prefetch_l2_bulk(args.codes[sh] + at, (uint32_t)min((int64_t)PF_BYTES, end - at));
+    };
+    auto row_block_of = [&](const Mx4Tile& t, int sh) {
+      return (sh || !GROUPED ? 0 : t.g * (args.rows[0] / 128)) + t.nb;
+    };
+    if (PREFETCH && cid < total) {
+      const Mx4Tile t = tile_of(cid);
+      const int sh = GROUPED && t.g == E ? 1 : 0;
+      for (int i = lane; i < (args.kt[sh] + KG - 1) / KG; i += 32)
+        prefetch_codes(sh, row_block_of(t, sh), i);
+      __syncwarp();
+    }
     // Test hook: the first stage is neither signalled nor loaded, so that the
     // MMA issuer's wait on it runs out.
     const int skip = (args.flags & MOE_FLAG_TEST_SKIP_SIGNAL) != 0 ? 1 : 0;
@@ -338,27 +436,45 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, KG, EG>::THRE
       const int kt = args.kt[sh];
       // The last row block of a pair may lie past the group's rows: it loads
       // what is there (another group's rows, or zeros) and stores nothing.
-      const int rt = uniform((sh || !GROUPED ? 0 : t.g * (args.rows[0] / 128)) + t.nb);
+      const int rt = uniform(row_block_of(t, sh));
       const int need = uniform(mma_cols(t) / CL);
-      const int bsel = need <= C::BOX2 ? 2 : (need <= C::BOX1 ? 1 : 0);
+      const int bsel = !PAIR || need > C::BOX1 ? 0 : (need > C::BOX2 ? 1 : 2);
       const int box = bsel == 2 ? C::BOX2 : (bsel == 1 ? C::BOX1 : C::B_ROWS);
       const uint32_t tx = CL * (C::A_TX + box * 128);
       const int b_row = uniform(t.p0) + crank * need;
       const CUtensorMap *mA = &args.tmA[sh], *mB = &args.tmB[sh][bsel];
-      const CUtensorMap *mSA = &args.tmSA[sh], *mSB = &args.tmSB[sh];
       const int sa_row = rt * kt, sb_row = uniform((int)t.tb) * kt * C::RA;
       const int sg0 = uniform(t.sg0), sg1 = uniform(t.sg1);
+      int next_sh = 0, next_rt = 0;
+      const bool has_next = PREFETCH && u + ncl < total;
+      if (has_next) {
+        const Mx4Tile n = tile_of(u + ncl);
+        next_sh = GROUPED && n.g == E ? 1 : 0;
+        next_rt = row_block_of(n, next_sh);
+      }
       for (int sg = sg0; sg < sg1; ++sg) {
         if (!(ok = warp_wait(sfempty_bar(ss), sph, args.status, limit))) break;
+        const int kend = min(kt, (sg + 1) * KG);
         if (el) {
           const uint32_t dst = sfs_base + (uint32_t)(ss * C::SF_BYTES);
-          if (leader) mbar_arrive_expect_tx(sffull_bar(ss), (uint32_t)(CL * C::SF_BYTES));
-          load(dst, mSA, 0, sa_row + sg * KG, 2 * STAGES + ss, pol_w);
-          load(dst + C::SA_BYTES, mSB, 0, sb_row + sg * KG * C::RA, 2 * STAGES + ss, pol_t);
+          if constexpr (PAIR) {
+            // Whole boxes: tiles past the matrix are zeros or never copied on.
+            if (leader) mbar_arrive_expect_tx(sffull_bar(ss), (uint32_t)(CL * C::SF_BYTES));
+            load(dst, &args.tmSA[sh], 0, sa_row + sg * KG, 2 * STAGES + ss, pol_w);
+            load(dst + C::SA_BYTES, &args.tmSB[sh], 0, sb_row + sg * KG * C::RA, 2 * STAGES + ss,
+                 pol_t);
+          } else {
+            const uint32_t n = (uint32_t)(kend - sg * KG) * 512u;
+            mbar_arrive_expect_tx(sffull_bar(ss), n * (1 + C::RA));
+            bulk_load(dst, args.sA[sh] + ((int64_t)sa_row + sg * KG) * 512, n, sffull_bar(ss),
+                      pol_w);
+            bulk_load(dst + C::SA_BYTES, args.sB[sh] + ((int64_t)sb_row + sg * KG * C::RA) * 512,
+                      n * C::RA, sffull_bar(ss), pol_t);
+            if (has_next) prefetch_codes(next_sh, next_rt, sg);
+          }
         }
         ++sit;
         if (++ss == C::SF_STAGES) ss = 0, sph ^= 1u;
-        const int kend = min(kt, (sg + 1) * KG);
         for (int ks = sg * KG + first; ks < kend; ks += C::KT_STAGE) {
           if (!(ok = warp_wait(empty_bar(s), ph, args.status, limit))) break;
           if (el) {
@@ -374,6 +490,29 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, KG, EG>::THRE
         first = 0;
         if (!ok) break;
       }
+    }
+    if (MODE == kGatedMx4 && PREFETCH && args.next_codes) {
+      // The down GEMM's unit cid: the same groups in the same order (no heavy
+      // ones), next_blocks row blocks each instead of rows / 128.
+      const int nf = args.rows[0] / 128;
+      int lo = 0, hi = ngroups;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if ((int64_t)prefix[mid] / nf * args.next_blocks <= cid) lo = mid;
+        else hi = mid;
+      }
+      if (ngroups > 0 && heavy_units == 0) {
+        const int g = order[lo];
+        const int mtiles = (offs[g + 1] - offs[g] + BN - 1) / BN;
+        const int nb = (cid - prefix[lo] / nf * args.next_blocks) / mtiles;
+        if (g < E && nb < args.next_blocks) {
+          const int64_t bytes = (int64_t)args.next_kt * 8192;
+          const uint8_t* p = args.next_codes + ((int64_t)g * args.next_blocks + nb) * bytes;
+          for (int64_t o = (int64_t)lane * 16384; o < bytes; o += 32 * 16384)
+            prefetch_l2_bulk(p + o, (uint32_t)min((int64_t)16384, bytes - o));
+        }
+      }
+      __syncwarp();
     }
     // Let the last loads land before the CTA (pair) can exit.
     if (el && leader) {
@@ -540,6 +679,16 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, KG, EG>::THRE
             }
           }
         }
+      } else if constexpr (SPLIT) {
+        // Partial sums to shared memory ([column][row], over the drained ring);
+        // the cluster adds them below.
+        float* part = reinterpret_cast<float*>(stages);
+        for (int c0 = 32 * eg; c0 < t.n_valid; c0 += 32 * EG) {
+          float v[32];
+          tmem_ld32(t_acc + c0, v);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) part[(c0 + i) * 128 + q * 32 + lane] = v[i];
+        }
       } else {
         // 32 columns at a time through shared memory: lanes hold weight rows,
         // and both epilogues want several rows of one token in a thread.
@@ -596,42 +745,15 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, KG, EG>::THRE
                     (uint16_t)(bytes[0] | (bytes[1] << 8));
             }
           } else {
-            const int N = args.rows[0];
             if (j < t.n_valid) {
-              const int64_t row = (int64_t)t.split * args.T + t.p0 + j;
 #pragma unroll
               for (int b = 0; b < 4; ++b) {
-                const int n0 = t.nb * 128 + b * 32 + fg * 8;
                 float o[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) o[i] = stage[(b * 32 + fg * 8 + i) * 33 + jj];
-                if (args.out_f32) {
-                  float* dst = reinterpret_cast<float*>(args.out) + row * args.ld_out + n0;
-                  if (args.vec_out && n0 + 8 <= N) {
-                    reinterpret_cast<float4*>(dst)[0] = make_float4(o[0], o[1], o[2], o[3]);
-                    reinterpret_cast<float4*>(dst)[1] = make_float4(o[4], o[5], o[6], o[7]);
-                  } else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                      if (n0 + i < N) dst[i] = o[i];
-                  }
-                } else {
-                  __nv_bfloat16* dst =
-                      reinterpret_cast<__nv_bfloat16*>(args.out) + row * args.ld_out + n0;
-                  if (args.vec_out && n0 + 8 <= N) {
-                    uint32_t w[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                      const __nv_bfloat162 p = __floats2bfloat162_rn(o[2 * i], o[2 * i + 1]);
-                      w[i] = *reinterpret_cast<const uint32_t*>(&p);
-                    }
-                    *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-                  } else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                      if (n0 + i < N) dst[i] = __float2bfloat16_rn(o[i]);
-                  }
-                }
+                store_outputs(o, args.out, (int64_t)(t.p0 + j) * args.ld_out,
+                              t.nb * 128 + b * 32 + fg * 8, args.rows[0], args.out_f32 != 0,
+                              args.vec_out != 0);
               }
             }
           }
@@ -651,10 +773,31 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, KG, EG>::THRE
   }
 
   tc_fence_before();
-  if constexpr (PAIR)
+  if constexpr (PAIR || SPLIT)
     cluster_sync();
   else
     __syncthreads();
+  if constexpr (SPLIT) {
+    // Each CTA adds its share of the tile's outputs over the cluster's partial
+    // sums, in the order of K.
+    const Mx4Tile t = tile_of(cid);
+    const int quads = t.n_valid * 32;  // 4 rows of one column each
+    const int per = (quads + splits - 1) / splits;
+    const int q0 = (int)cluster_ctarank() * per, q1 = min(quads, q0 + per);
+    for (int i = q0 + (int)threadIdx.x; i < q1; i += C::THREADS) {
+      const uint32_t at = stages_base + (uint32_t)i * 16u;
+      float4 a = ld_cluster_f4(mapa_shared(at, 0));
+      for (int k = 1; k < splits; ++k) {
+        const float4 b = ld_cluster_f4(mapa_shared(at, (uint32_t)k));
+        a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
+      }
+      const float o[4] = {a.x, a.y, a.z, a.w};
+      store_outputs(o, args.out, (int64_t)(t.p0 + i / 32) * args.ld_out,
+                    t.nb * 128 + (i % 32) * 4, args.rows[0], args.out_f32 != 0,
+                    args.vec_out != 0);
+    }
+    cluster_sync();  // no CTA leaves while a peer reads its sums
+  }
   if (warp == 1) {
     tc_fence_after();
     if constexpr (PAIR)
@@ -664,52 +807,45 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, KG, EG>::THRE
   }
 }
 
-// y[t][n] = sum over the splits of the partial sums, in split order.
-template <typename TOut>
-__global__ void __launch_bounds__(256) split_sum_kernel(const float* __restrict__ part, int T,
-                                                        int N, int splits, TOut* __restrict__ y,
-                                                        int64_t ld) {
-  pdl_entry();
-  const int64_t n = (int64_t)T * N;
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n;
-       i += (int64_t)gridDim.x * blockDim.x) {
-    float s = part[i];
-    for (int k = 1; k < splits; ++k) s += part[i + k * n];
-    const int64_t t = i / N;
-    if constexpr (sizeof(TOut) == 2)
-      y[t * ld + (i - t * N)] = __float2bfloat16_rn(s);
-    else
-      y[t * ld + (i - t * N)] = s;
-  }
-}
-
 constexpr int kMaxExperts = 1024;  // the C ABI's limit on E
-// Token tiles: 64 rows on single CTAs (7 stages of 24 KB), 224 rows on pairs (5
-// or 6 stages of 30 KB; two accumulators of 224 columns and the scales fill
-// tensor memory).
-constexpr int kSmallTile = 64, kPairTile = 224;
 constexpr int kScaleGroup = 4;  // k tiles per scale load (KG)
+constexpr int kPairTile = 224;
 
-template <int MODE, bool F4, int CL, int BN, int STAGES, int KG, int EG>
-cudaError_t launch_variant(const Mx4Args& a, int num_sms, size_t units, cudaStream_t st) {
-  using C = Mx4Cfg<MODE, F4, CL, BN, STAGES, KG, EG>;
+template <int MODE, bool F4, int CL, int BN, int STAGES, int KG, int EG, bool SPLIT>
+cudaError_t launch_variant(const Mx4Args& a, int num_sms, size_t units, int splits,
+                           cudaStream_t st) {
+  using C = Mx4Cfg<MODE, F4, CL, BN, STAGES, KG, EG, SPLIT>;
   static_assert(CL == 1 || CL == 2, "single CTAs or pairs");
-  auto fn = mx4_gemm_kernel<MODE, F4, CL, BN, STAGES, KG, EG>;
+  auto fn = mx4_gemm_kernel<MODE, F4, CL, BN, STAGES, KG, EG, SPLIT>;
   cudaError_t e = ensure_smem_attr((const void*)fn, C::smem_bytes(kMaxExperts));
   if (e != cudaSuccess) return e;
+  if (units == 0) return cudaSuccess;
   size_t n = (size_t)(num_sms / CL);
-  if (units < n) n = units;
-  if (n == 0) return cudaSuccess;
-  return launch_chained(fn, dim3((unsigned)(n * CL)), dim3(C::THREADS), C::smem_bytes(a.E), st,
-                        CL, a);
+  if (SPLIT || units < n) n = units;  // a split tile is one cluster's only unit
+  const size_t cluster = (size_t)(CL * (SPLIT ? splits : 1));
+  return launch_chained(fn, dim3((unsigned)(n * cluster)), dim3(C::THREADS), C::smem_bytes(a.E),
+                        st, (unsigned)cluster, a);
 }
 
+// Token tiles: 32 or 64 rows on single CTAs (9 stages of 20 KB, 7 of 24 KB), 224
+// rows on pairs (5 or 6 stages of 30 KB; two accumulators of 224 columns and
+// the scales fill tensor memory).
 template <int MODE, bool F4>
-cudaError_t launch_mx4(const Mx4Args& a, bool pairs, int num_sms, size_t units, cudaStream_t st) {
-  if (!pairs)
-    return launch_variant<MODE, F4, 1, kSmallTile, 7, kScaleGroup, 1>(a, num_sms, units, st);
-  return launch_variant<MODE, F4, 2, kPairTile, MODE == kDownMx4 ? 6 : 5, kScaleGroup, 2>(
-      a, num_sms, units, st);
+cudaError_t launch_mx4(const Mx4Args& a, const Mx4Tiling& t, int num_sms, size_t units, int splits,
+                       cudaStream_t st) {
+  constexpr int KG = kScaleGroup;
+  if (t.pairs)
+    return launch_variant<MODE, F4, 2, kPairTile, MODE == kDownMx4 ? 6 : 5, KG, 2, false>(
+        a, num_sms, units, 1, st);
+  if constexpr (MODE == kLinearMx4) {
+    if (splits > 1)
+      return t.rows == 32
+                 ? launch_variant<MODE, F4, 1, 32, 9, KG, 1, true>(a, num_sms, units, splits, st)
+                 : launch_variant<MODE, F4, 1, 64, 7, KG, 1, true>(a, num_sms, units, splits, st);
+    if (t.rows == 64)
+      return launch_variant<MODE, F4, 1, 64, 7, KG, 1, false>(a, num_sms, units, 1, st);
+  }
+  return launch_variant<MODE, F4, 1, 32, 9, KG, 1, false>(a, num_sms, units, 1, st);
 }
 
 struct TokenMaps {
@@ -719,37 +855,39 @@ struct TokenMaps {
   uint64_t tiles;  // token tiles of the scales
 };
 
-template <bool F4, int CL, int BN>
-bool make_token_maps_of(CUtensorMap (&m)[3], CUtensorMap* ms, const TokenMaps& t) {
-  constexpr int KG = kScaleGroup;
-  using C = Mx4Cfg<kDownMx4, F4, CL, BN, 4, KG, 1>;
+// Operand maps and addresses of group kind i (0 routed, 1 shared).
+template <bool F4>
+bool set_tokens(Mx4Args& a, int i, const TokenMaps& t, const Mx4Tiling& tl) {
   const uint64_t cols = (uint64_t)t.kt * (F4 ? 64 : 128);
-  return make_tma_map(&m[0], t.q, MOE_DTYPE_E4M3, t.rows, cols, C::B_ROWS) &&
-         make_tma_map(&m[1], t.q, MOE_DTYPE_E4M3, t.rows, cols, C::BOX1) &&
-         make_tma_map(&m[2], t.q, MOE_DTYPE_E4M3, t.rows, cols, C::BOX2) &&
-         make_scale_tile_map(ms, t.s, t.tiles * t.kt * C::RA, KG * C::RA);
+  a.sB[i] = t.s;
+  if (!tl.pairs) return make_tma_map(&a.tmB[i][0], t.q, MOE_DTYPE_E4M3, t.rows, cols, tl.rows);
+  using C = Mx4Cfg<kDownMx4, F4, 2, kPairTile, 4, kScaleGroup, 1, false>;
+  return make_tma_map(&a.tmB[i][0], t.q, MOE_DTYPE_E4M3, t.rows, cols, C::B_ROWS) &&
+         make_tma_map(&a.tmB[i][1], t.q, MOE_DTYPE_E4M3, t.rows, cols, C::BOX1) &&
+         make_tma_map(&a.tmB[i][2], t.q, MOE_DTYPE_E4M3, t.rows, cols, C::BOX2) &&
+         make_scale_tile_map(&a.tmSB[i], t.s, t.tiles * t.kt * C::RA, kScaleGroup * C::RA);
 }
 
 template <bool F4>
-bool make_token_maps(CUtensorMap (&m)[3], CUtensorMap* ms, const TokenMaps& t, bool pairs) {
-  return pairs ? make_token_maps_of<F4, 2, kPairTile>(m, ms, t)
-               : make_token_maps_of<F4, 1, kSmallTile>(m, ms, t);
-}
-
-template <bool F4>
-bool make_weight_maps(CUtensorMap* m, CUtensorMap* ms, const uint8_t* q, const uint8_t* s,
-                      uint64_t rows, int kt) {
-  const bool ok = F4 ? make_tma_map(m, q, MOE_DTYPE_E4M3, rows, (uint64_t)kt * 64, 128)
-                     : make_spread_code_map(m, q, rows, (uint64_t)kt * 128, 128);
-  return ok && make_scale_tile_map(ms, s, (rows + 127) / 128 * kt, kScaleGroup);
+bool set_weights(Mx4Args& a, int i, const uint8_t* q, const uint8_t* s, uint64_t rows,
+                 const Mx4Tiling& tl) {
+  const int kt = a.kt[i];
+  a.sA[i] = s;
+  a.codes[i] = q;
+  a.code_bytes[i] = (int64_t)rows * kt * 64;
+  const bool ok = F4 ? make_tma_map(&a.tmA[i], q, MOE_DTYPE_E4M3, rows, (uint64_t)kt * 64, 128)
+                     : make_spread_code_map(&a.tmA[i], q, rows, (uint64_t)kt * 128, 128);
+  return ok &&
+         (!tl.pairs || make_scale_tile_map(&a.tmSA[i], s, (rows + 127) / 128 * kt, kScaleGroup));
 }
 
 }  // namespace
 
+// Grouped products: 32-row tiles up to 64 tokens (or when forced), pairs above.
 Mx4Tiling mx4_tiling(int64_t T, int tile) {
   const bool pairs = tile == MOE_TILE_MEDIUM || tile == MOE_TILE_PREFILL ||
-                     (tile == MOE_TILE_AUTO && T > kSmallTile);
-  return pairs ? Mx4Tiling{true, kPairTile, 32, 2} : Mx4Tiling{false, kSmallTile, 16, 1};
+                     (tile == MOE_TILE_AUTO && T > 64);
+  return pairs ? Mx4Tiling{true, kPairTile, 32, 2} : Mx4Tiling{false, 32, 16, 1};
 }
 
 namespace {
@@ -773,21 +911,24 @@ cudaError_t launch_grouped(const GemmProblem& p, const Mx4Weights& w, const Mx4T
                         (uint64_t)group_scale_tile(P, p.E, bn) + 1};
   const TokenMaps sh = {x.shared, x.shared_s, (uint64_t)p.T, a.kt[1],
                         (uint64_t)((p.T + bn - 1) / bn)};
-  bool ok = make_weight_maps<false>(&a.tmA[0], &a.tmSA[0], GATED ? w.gate_up : w.down,
-                                        GATED ? w.s_gate_up : w.s_down,
-                                        (uint64_t)p.E * a.rows[0], a.kt[0]) &&
-            make_token_maps<false>(a.tmB[0], &a.tmSB[0], rt, tl.pairs);
+  bool ok = set_weights<false>(a, 0, GATED ? w.gate_up : w.down, GATED ? w.s_gate_up : w.s_down,
+                               (uint64_t)p.E * a.rows[0], tl) &&
+            set_tokens<false>(a, 0, rt, tl);
   if (ok && has_s)
-    ok = make_weight_maps<false>(&a.tmA[1], &a.tmSA[1], GATED ? w.sh_gate_up : w.sh_down,
-                                     GATED ? w.sh_s_gate_up : w.sh_s_down, (uint64_t)a.rows[1],
-                                     a.kt[1]) &&
-         make_token_maps<false>(a.tmB[1], &a.tmSB[1], sh, tl.pairs);
+    ok = set_weights<false>(a, 1, GATED ? w.sh_gate_up : w.sh_down,
+                            GATED ? w.sh_s_gate_up : w.sh_s_down, (uint64_t)a.rows[1], tl) &&
+         set_tokens<false>(a, 1, sh, tl);
   if (!ok) return cudaErrorInvalidValue;
   if (!has_s) {
     a.tmA[1] = a.tmA[0];
     a.tmSA[1] = a.tmSA[0];
     a.tmSB[1] = a.tmSB[0];
     for (int i = 0; i < 3; ++i) a.tmB[1][i] = a.tmB[0][i];
+  }
+  if (GATED && !has_s) {
+    a.next_codes = w.down;
+    a.next_blocks = p.H / 128;
+    a.next_kt = p.I / 128;
   }
   a.offsets = offsets;
   a.gather_idx = gather_idx;
@@ -806,7 +947,7 @@ cudaError_t launch_grouped(const GemmProblem& p, const Mx4Weights& w, const Mx4T
   const int ur = tl.pairs ? 256 : 128;  // weight rows of a unit
   const size_t ub = unit_upper_bound(p.T, p.k, p.E, bn, (a.rows[0] + ur - 1) / ur,
                                      has_s ? (a.rows[1] + ur - 1) / ur : 0);
-  return launch_mx4<MODE, false>(a, tl.pairs, p.num_sms, ub, st);
+  return launch_mx4<MODE, false>(a, tl, p.num_sms, ub, 1, st);
 }
 
 }  // namespace
@@ -823,12 +964,20 @@ cudaError_t launch_mx4_down_gemm(const GemmProblem& p, const Mx4Weights& w, cons
   return launch_grouped<kDownMx4>(p, w, h, offsets, gather_idx, topk_w, Mx4Out{}, Y, status, st);
 }
 
-int mx4_linear_splits(int T, int64_t N, int64_t K, int num_sms) {
-  (void)T;
-  (void)N;
-  (void)K;
-  (void)num_sms;
-  return 1;
+// Tiling and clusters over K of a dense product.
+Mx4LinearPlan mx4_linear_plan(int64_t T, int64_t N, int64_t K, int num_sms) {
+  const int64_t sg = (mxfp4_k_tiles(K) + kScaleGroup - 1) / kScaleGroup;
+  const int64_t blocks = (N + 127) / 128;
+  // Pairs when they fill at least half of the GPU.
+  const int64_t pair_units = (blocks + 1) / 2 * ((T + kPairTile - 1) / kPairTile);
+  if (T > 64 && pair_units * 4 >= num_sms) return {{true, kPairTile, 32, 2}, 1};
+  const int rows = T <= 32 ? 32 : 64;
+  const int64_t units = blocks * ((T + rows - 1) / rows);
+  // As many CTAs per tile as still fit the GPU at once and leave each at least
+  // two scale groups (1024 of K).
+  int splits = 1;
+  while (splits < 8 && units * splits * 2 <= num_sms && sg >= 4 * splits) splits *= 2;
+  return {{false, rows, 16, 1}, splits};
 }
 
 cudaError_t launch_mx4_linear(const Mx4Linear& l, cudaStream_t st) {
@@ -836,45 +985,26 @@ cudaError_t launch_mx4_linear(const Mx4Linear& l, cudaStream_t st) {
   memset(&a, 0, sizeof(a));
   a.kt[0] = a.kt[1] = (int)mxfp4_k_tiles(l.K);
   a.rows[0] = a.rows[1] = (int)l.N;
-  const Mx4Tiling tl = mx4_tiling(l.T, MOE_TILE_AUTO);
-  const int bn = tl.rows;
-  const TokenMaps tm = {l.xq, l.xs, (uint64_t)l.T, a.kt[0], (uint64_t)((l.T + bn - 1) / bn)};
-  const bool ok =
-      l.e2m1 ? make_weight_maps<true>(&a.tmA[0], &a.tmSA[0], l.wq, l.ws, l.N, a.kt[0]) &&
-                   make_token_maps<true>(a.tmB[0], &a.tmSB[0], tm, tl.pairs)
-             : make_weight_maps<false>(&a.tmA[0], &a.tmSA[0], l.wq, l.ws, l.N, a.kt[0]) &&
-                   make_token_maps<false>(a.tmB[0], &a.tmSB[0], tm, tl.pairs);
+  const Mx4Tiling& tl = l.plan.tiling;
+  const TokenMaps tm = {l.xq, l.xs, (uint64_t)l.T, a.kt[0],
+                        (uint64_t)((l.T + tl.rows - 1) / tl.rows)};
+  const bool ok = l.e2m1 ? set_weights<true>(a, 0, l.wq, l.ws, l.N, tl) &&
+                               set_tokens<true>(a, 0, tm, tl)
+                         : set_weights<false>(a, 0, l.wq, l.ws, l.N, tl) &&
+                               set_tokens<false>(a, 0, tm, tl);
   if (!ok) return cudaErrorInvalidValue;
-  a.tmA[1] = a.tmA[0];
-  a.tmSA[1] = a.tmSA[0];
-  a.tmSB[1] = a.tmSB[0];
-  for (int i = 0; i < 3; ++i) a.tmB[1][i] = a.tmB[0][i];
   a.status = l.status;
   a.limit_ns = l.limit_ns;
   a.T = l.T;
-  a.splits = l.splits;
-  const int sg = (a.kt[0] + kScaleGroup - 1) / kScaleGroup;
-  a.groups_per_split = (sg + l.splits - 1) / l.splits;
-  a.splits = (sg + a.groups_per_split - 1) / a.groups_per_split;  // no empty split
-  const bool part = a.splits > 1;
-  a.out = part ? (void*)l.part : l.y;
-  a.ld_out = part ? l.N : l.ld_y;
-  a.out_f32 = part || l.y_f32;
-  const int es = a.out_f32 ? 4 : 2;
-  a.vec_out = (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0 && a.ld_out * es % 16 == 0;
+  a.out = l.y;
+  a.ld_out = l.ld_y;
+  a.out_f32 = l.y_f32;
+  a.vec_out = (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0 &&
+              a.ld_out * (l.y_f32 ? 4 : 2) % 16 == 0;
   const int ur = tl.pairs ? 256 : 128;  // weight rows of a unit
-  const size_t units = (size_t)((l.N + ur - 1) / ur) * ((l.T + bn - 1) / bn) * a.splits;
-  cudaError_t e = l.e2m1 ? launch_mx4<kLinearMx4, true>(a, tl.pairs, l.num_sms, units, st)
-                         : launch_mx4<kLinearMx4, false>(a, tl.pairs, l.num_sms, units, st);
-  if (e != cudaSuccess || !part) return e;
-  int64_t blocks = ((int64_t)l.T * l.N + 255) / 256;
-  if (blocks > 8 * (int64_t)l.num_sms) blocks = 8 * (int64_t)l.num_sms;
-  if (l.y_f32)
-    return launch_chained(split_sum_kernel<float>, dim3((unsigned)blocks), dim3(256), 0, st, 1,
-                          (const float*)l.part, l.T, (int)l.N, a.splits, (float*)l.y, l.ld_y);
-  return launch_chained(split_sum_kernel<__nv_bfloat16>, dim3((unsigned)blocks), dim3(256), 0, st,
-                        1, (const float*)l.part, l.T, (int)l.N, a.splits, (__nv_bfloat16*)l.y,
-                        l.ld_y);
+  const size_t units = (size_t)((l.N + ur - 1) / ur) * ((l.T + tl.rows - 1) / tl.rows);
+  return l.e2m1 ? launch_mx4<kLinearMx4, true>(a, tl, l.num_sms, units, l.plan.splits, st)
+                : launch_mx4<kLinearMx4, false>(a, tl, l.num_sms, units, l.plan.splits, st);
 }
 
 }  // namespace moe

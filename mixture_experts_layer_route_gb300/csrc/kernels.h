@@ -215,7 +215,8 @@ cudaError_t launch_quantize_mxfp4(int dtype, const void* src, const void* src2, 
 cudaError_t launch_dequantize_mxfp4(const uint8_t* q, const uint8_t* scales, int64_t rows,
                                     int64_t cols, int dtype, void* out, int64_t ld, int num_sms,
                                     cudaStream_t st);
-// Token tiles of an MXFP4 product (gemm_mxfp4.cu): at most `rows` rows, cut in
+// Token tiles of an MXFP4 product (gemm_mxfp4.cu; mx4_tiling: of the layer's
+// grouped ones): at most `rows` rows, cut in
 // multiples of `unit`, with `row_atoms` 128-row scale tiles each.
 struct Mx4Tiling {
   bool pairs;  // CTA pairs (cta_group::2)
@@ -236,6 +237,7 @@ struct MxTokenArgs {
   uint8_t *shared_q, *shared_s;
   const int32_t *slot_pos, *topk_ids, *offsets;
   int* status;
+  int clear_status;  // set *status to MOE_OK (the first kernel of its call)
 };
 cudaError_t launch_quantize_tokens(const MxTokenArgs& args, bool routed, bool e2m1,
                                    cudaStream_t st);
@@ -258,18 +260,22 @@ cudaError_t launch_mx4_swiglu_gemm(const GemmProblem& p, const Mx4Weights& w, co
 cudaError_t launch_mx4_down_gemm(const GemmProblem& p, const Mx4Weights& w, const Mx4Tokens& h,
                                  const int32_t* offsets, const int32_t* gather_idx,
                                  const float* topk_w, float* Y, int* status, cudaStream_t st);
-// y [T][N] = x W^T. splits > 1: fp32 partial sums [splits][T][N] in part,
-// added in split order.
-int mx4_linear_splits(int T, int64_t N, int64_t K, int num_sms);
+// y [T][N] = x W^T; splits > 1: clusters of that many CTAs share a tile, each
+// with a range of K.
+struct Mx4LinearPlan {
+  Mx4Tiling tiling;
+  int splits;
+};
+Mx4LinearPlan mx4_linear_plan(int64_t T, int64_t N, int64_t K, int num_sms);
 struct Mx4Linear {
   int T;
   int64_t N, K;
   bool e2m1, y_f32;
+  Mx4LinearPlan plan;
   const uint8_t *xq, *xs, *wq, *ws;
   void* y;
   int64_t ld_y;
-  float* part;
-  int splits, num_sms;
+  int num_sms;
   int* status;
   unsigned long long limit_ns;
 };

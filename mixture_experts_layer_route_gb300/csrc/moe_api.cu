@@ -991,12 +991,11 @@ moe_status moe_dequantize_mxfp4(const uint8_t* q, const uint8_t* scales, int64_t
 namespace {
 
 struct LinearLayout {
-  size_t xq, xs, part, total;
-  int splits;
+  size_t xq, xs, total;
+  Mx4LinearPlan plan;
 };
 
-// Workspace of moe_linear_mxfp4: status word, token codes, scale tiles, and
-// the partial sums of a split contraction.
+// Workspace of moe_linear_mxfp4: status word, token codes, scale tiles.
 LinearLayout linear_layout(int64_t T, int64_t N, int64_t K, bool e2m1) {
   LinearLayout L;
   size_t off = kHeader;
@@ -1005,10 +1004,12 @@ LinearLayout linear_layout(int64_t T, int64_t N, int64_t K, bool e2m1) {
     off = align_up(off + bytes);
     return o;
   };
+  // The plan of a fixed SM count keeps the size independent of the device.
+  L.plan = mx4_linear_plan(T, N, K, kRouterSplitSms);
+  const Mx4Tiling& t = L.plan.tiling;
   L.xq = take((size_t)T * (size_t)mxfp4_k_tiles(K) * (e2m1 ? 64 : 128));
-  L.xs = take(mx4_token_scale_bytes(T, MOE_TILE_AUTO, K));
-  L.splits = mx4_linear_splits((int)T, N, K, kRouterSplitSms);
-  L.part = L.splits > 1 ? take((size_t)L.splits * (size_t)T * (size_t)N * 4) : 0;
+  L.xs = take((size_t)((T + t.rows - 1) / t.rows) * (size_t)mxfp4_k_tiles(K) *
+              (size_t)t.row_atoms * 512);
   L.total = off;
   return L;
 }
@@ -1055,15 +1056,17 @@ moe_status moe_linear_mxfp4(const void* x, int64_t T, int64_t K, int64_t ld_x, i
   if ((s = check_ws(workspace, workspace_bytes, L.total)) != MOE_OK) return s;
   if (!tensor_map_encoder_available()) return MOE_ERR_UNSUPPORTED;
   cudaStream_t st = (cudaStream_t)stream;
-  cudaError_t e = cudaMemsetAsync(workspace, 0, sizeof(int), st);
-  if (e == cudaSuccess) {
+  cudaError_t e;
+  {
     NvtxRange r("quantize_x");
     MxTokenArgs a = {};
+    a.status = status_ptr(workspace);
+    a.clear_status = 1;
     a.x = x;
     a.ld = ld_x;
     a.T = (int)T;
     a.K = (int)K;
-    a.tiling = mx4_tiling(T, MOE_TILE_AUTO);
+    a.tiling = L.plan.tiling;
     a.q = at<uint8_t>(workspace, L.xq);
     a.s = at<uint8_t>(workspace, L.xs);
     e = launch_quantize_tokens(a, false, e2m1, st);
@@ -1082,8 +1085,7 @@ moe_status moe_linear_mxfp4(const void* x, int64_t T, int64_t K, int64_t ld_x, i
     l.ws = s_W;
     l.y = y;
     l.ld_y = ld_y;
-    l.part = L.splits > 1 ? at<float>(workspace, L.part) : nullptr;
-    l.splits = L.splits;
+    l.plan = L.plan;
     l.num_sms = sm_count();
     l.status = status_ptr(workspace);
     l.limit_ns = 1000000000ull;

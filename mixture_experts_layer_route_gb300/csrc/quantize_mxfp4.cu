@@ -275,6 +275,7 @@ __global__ void __launch_bounds__(256) quantize_tokens_kernel(MxTokenArgs a) {
       dest[threadIdx.x] = d;
     }
   }
+  if (!ROUTED && a.clear_status && blockIdx.x == 0 && threadIdx.x == 0) *a.status = MOE_OK;
   if (threadIdx.x == 32) {  // the row in token order
     const int tn = token_tile_rows(a.T, a.tiling.rows, a.tiling.unit);
     const int mt = t / tn;

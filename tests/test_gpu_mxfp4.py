@@ -116,7 +116,7 @@ def _check_linear(x, W, act, lin=None):
     return lin, y
 
 
-LINEAR = [(1, 128, 128), (1, 4096, 4096), (3, 1, 1), (16, 200, 130), (17, 129, 416), (33, 640, 1056),
+LINEAR = [(1, 128, 128), (2, 300, 4500), (40, 500, 9216), (1, 4096, 4096), (3, 1, 1), (16, 200, 130), (17, 129, 416), (33, 640, 1056),
           (64, 256, 2048), (65, 384, 160), (200, 131, 640), (333, 1000, 1440), (450, 512, 96),
           (1000, 260, 288)]
 

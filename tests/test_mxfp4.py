@@ -65,6 +65,9 @@ def test_reference_layout():
 
 def test_storage_sizes(lib):
     assert [m.mxfp4_code_cols(c) for c in (1, 128, 129, 4096)] == [64, 64, 128, 2048]
+    for r, c in ((1, 1), (127, 4095), (129, 129), (1000, 1440)):
+        assert lib.moe_mxfp4_code_cols(c) == m.mxfp4_code_cols(c)
+        assert lib.moe_mxfp4_scale_bytes(r, c) == m.mxfp4_scale_bytes(r, c)
     assert [m.mxfp4_scale_bytes(r, c) for r, c in ((1, 1), (128, 128), (129, 128), (256, 4096))] == [
         512, 512, 1024, 2 * 32 * 512]
 
