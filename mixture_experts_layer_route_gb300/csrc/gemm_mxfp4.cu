@@ -168,7 +168,9 @@ __device__ __forceinline__ bool elect_lane() {
   return r != 0;
 }
 
-__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+// A value that all lanes hold, through a warp reduction: the result is known to
+// be uniform at compile time, and so is control flow that depends on it.
+__device__ __forceinline__ int uniform(int v) { return __reduce_max_sync(0xffffffffu, v); }
 
 // mbar_wait by a whole warp, with one answer for all of its lanes.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int* status,
@@ -332,16 +334,16 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, KG, EG, SPLIT
   __syncthreads();
   if constexpr (PAIR) cluster_sync();
   tc_fence_after();
-  const uint32_t tmem_base = *tmem_holder;
+  const uint32_t tmem_base = (uint32_t)uniform((int)*tmem_holder);
   const uint32_t sf_cols = tmem_base + 2 * BN;
   const uint64_t limit = args.limit_ns;
 
   int ngroups = 0, heavy_units = 0, total;
   int lin_nb = 0, lin_mt = 0;
   if constexpr (GROUPED) {
-    ngroups = *n_sched;
-    heavy_units = *n_heavy;
-    total = prefix[ngroups];
+    ngroups = uniform(*n_sched);
+    heavy_units = uniform(*n_heavy);
+    total = uniform(prefix[ngroups]);
   } else {
     lin_nb = (args.rows[0] + 128 * CL - 1) / (128 * CL);
     lin_mt = (args.T + BN - 1) / BN;
@@ -432,7 +434,7 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, KG, EG, SPLIT
     bool ok = true;
     for (int u = cid; u < total && ok; u += ncl) {
       const Mx4Tile t = tile_of(u);
-      const int sh = GROUPED && t.g == E ? 1 : 0;
+      const int sh = GROUPED ? uniform(t.g == E) : 0;
       const int kt = args.kt[sh];
       // The last row block of a pair may lie past the group's rows: it loads
       // what is there (another group's rows, or zeros) and stores nothing.
@@ -544,7 +546,7 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, KG, EG, SPLIT
       bool ok = true;
       for (int u = cid; u < total && ok; u += ncl, ++lt) {
         const Mx4Tile t = tile_of(u);
-        const int kt = args.kt[GROUPED && t.g == E ? 1 : 0];
+        const int kt = args.kt[GROUPED ? uniform(t.g == E) : 0];
         const int sg0 = uniform(t.sg0), sg1 = uniform(t.sg1);
         const uint32_t acc = lt & 1u;
         if (!(ok = warp_wait(tempty_bar(acc), ((lt >> 1) & 1u) ^ 1u, args.status, limit))) break;
