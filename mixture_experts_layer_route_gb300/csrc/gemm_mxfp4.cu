@@ -13,24 +13,26 @@
 // rows a CTA), the tokens its N operand, so that ragged groups cost at most one
 // partly filled tile and a few tokens stream their weights with a narrow N.
 //
-// What the operands look like in shared memory (rows of 128 bytes, 128-byte
-// swizzle, K-major):
-//   E4M3 tokens: one k tile (128 elements) a stage. The weight codes are
+// A stage of the shared-memory ring holds NB boxes of both operands (rows of 128
+// bytes, 128-byte swizzle, K-major) and their scale tiles:
+//   E4M3 tokens: a box is one k tile (128 elements). The weight codes are
 //     spread to one code a byte position by the TMA load itself (16 codes to 8
 //     bytes of data and 8 of padding, the form kind::mxf8f6f4 reads), so 8 KB
-//     from memory fill 16 KB of a stage.
-//   E2M1 tokens (kind::mxf4): both operands packed, two k tiles a stage.
-// Scales travel in groups of KG k tiles through a ring of their own (one box
-// of KG 512-byte tiles for the weights, one of KG x RA for the tokens), so that
-// they cost two load instructions a group, and each stage's tiles are copied
-// into one of two column ranges of tensor memory by tcgen05.cp before its MMAs.
+//     from memory fill 16 KB.
+//   E2M1 tokens (kind::mxf4): both operands packed, two k tiles a box.
+// A box's scale tiles are copied into one of two column ranges of tensor memory
+// (tcgen05.cp) right before its four MMAs.
 //
-// The producer's and the issuer's loops are run by a whole warp with one
-// elected lane issuing: the operands of TMA and tcgen05 instructions are then
-// provably warp-uniform. A loop under `lane == 0` took 340 cycles for a
-// stage's four MMAs and ~130 for each scale copy; elected, four MMAs with two
-// copies take 212 at N <= 64 (8 KB of weights: 11 TB/s over the chip, above
-// HBM's rate), and the copies hide behind the MMAs.
+// What sets the pace is the issue of these instructions, ~30 cycles each, and
+// the ~130 of a barrier wait, against 4 x 63 cycles of MMA work a box at N <=
+// 128. Hence:
+//  - the producer's and the issuer's loops are run by a whole warp with one
+//    elected lane issuing, and every loop bound comes through a warp
+//    reduction, so that the operands are provably warp-uniform (a loop under
+//    `lane == 0` took 85 cycles per MMA and 130 per scale copy);
+//  - NB = 2: one wait and one commit for eight MMAs. One box a stage took 460
+//    cycles on the decode layer's gate/up GEMM, where HBM delivers its 8 KB in
+//    350.
 //
 // Warp roles: warp 0 TMA producer, warp 1 MMA issuer (one thread) and owner of
 // the tensor memory, the others epilogue (four per group, one 32-lane quarter
@@ -82,37 +84,39 @@ struct Mx4Args {
   int out_f32, vec_out;
 };
 
-template <int MODE, bool F4, int CL, int BN, int STAGES, int KG, int EG, bool SPLIT>
+template <int MODE, bool F4, int CL, int BN, int STAGES, int EG, bool SPLIT>
 struct Mx4Cfg {
-  static constexpr int KT_STAGE = F4 ? 2 : 1;          // k tiles per stage
+  static constexpr int NB = 2;                         // boxes per stage
+  static constexpr int KT_BOX = F4 ? 2 : 1;            // k tiles per box
+  static constexpr int KT_STAGE = NB * KT_BOX;
   static constexpr int RA = (BN + 127) / 128;          // 128-row scale tiles per token tile
-  static constexpr int A_BYTES = 128 * 128;
-  static constexpr int A_TX = F4 ? A_BYTES : A_BYTES / 2;  // bytes the load counts
+  static constexpr int A_BOX = 128 * 128;
+  static constexpr int A_TX = F4 ? A_BOX : A_BOX / 2;  // bytes the load counts
   static constexpr int B_ROWS = BN / CL;
   static constexpr int BOX1 = CL == 2 ? 64 : B_ROWS, BOX2 = CL == 2 ? 32 : B_ROWS;
   static constexpr int N_UNIT = 16 * CL;
-  static constexpr int B_BYTES = B_ROWS * 128;
-  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-  static constexpr int SA_BYTES = KG * 512, SB_BYTES = KG * RA * 512;
-  static constexpr int SF_BYTES = SA_BYTES + SB_BYTES;
-  static constexpr int SF_STAGES = 3;
-  // Tensor-memory columns of one stage's scales (two ranges, by stage parity).
-  static constexpr int SF_COLS = KT_STAGE * 4 * (1 + RA);
+  static constexpr int B_BOX = B_ROWS * 128;
+  static constexpr int B_OFF = NB * A_BOX;
+  static constexpr int SA_OFF = B_OFF + NB * B_BOX;
+  static constexpr int SA_BYTES = KT_STAGE * 512, SB_BYTES = KT_STAGE * RA * 512;
+  static constexpr int SB_OFF = SA_OFF + SA_BYTES;
+  static constexpr int STAGE_BYTES = SB_OFF + SB_BYTES;
+  // Tensor-memory columns of one box's scales (two ranges, by box parity).
+  static constexpr int SF_COLS = KT_BOX * 4 * (1 + RA);
   static constexpr int USED_COLS = 2 * BN + 2 * SF_COLS;
-  static constexpr int TMEM_COLS = USED_COLS <= 256 ? 256 : 512;
+  static constexpr int TMEM_COLS = USED_COLS <= 128 ? 128 : (USED_COLS <= 256 ? 256 : 512);
   static constexpr int EPI_GROUPS = EG;
   static constexpr int EPI_THREADS = 128 * EG;
   static constexpr int THREADS = 64 + EPI_THREADS;
   static constexpr int EPI_FLOATS = (MODE == kDownMx4 ? 0 : EG * 128 * 33) + 2 * BN;
-  // full, empty [STAGES]; sffull, sfempty [SF_STAGES]; tfull, tempty [2]; drain
-  static constexpr int NBARS = 2 * STAGES + 2 * SF_STAGES + 5;
+  // full, empty [STAGES]; tfull, tempty [2]; drain
+  static constexpr int NBARS = 2 * STAGES + 5;
   static_assert(!SPLIT || (MODE == kLinearMx4 && CL == 1), "clusters over K: dense, single CTAs");
   static_assert(USED_COLS <= 512, "tensor memory");
-  static_assert(STAGE_BYTES % 1024 == 0 && KG % KT_STAGE == 0, "stage");
+  static_assert(STAGE_BYTES % 1024 == 0 && B_BOX % 1024 == 0, "swizzled boxes start on 1 KB");
 
   static size_t smem_bytes(int E) {
-    return 1024 + (size_t)STAGES * STAGE_BYTES + (size_t)SF_STAGES * SF_BYTES + EPI_FLOATS * 4 +
-           NBARS * 8 + 16 + (MODE == kLinearMx4 ? 0 : 3 * (size_t)(E + 2) * 4);
+    return 1024 + (size_t)STAGES * STAGE_BYTES + EPI_FLOATS * 4 + NBARS * 8 + 16 + (MODE == kLinearMx4 ? 0 : 3 * (size_t)(E + 2) * 4);
   }
 };
 
@@ -188,10 +192,10 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int* st
 }
 
 // One unit of work of a CTA (pair): weight row block nb (of 128 rows; pairs
-// take 2 nb and 2 nb + 1) of group g on one token tile, over scale groups
-// [sg0, sg1) of the contraction.
+// take 2 nb and 2 nb + 1) of group g on one token tile, over stages [s0, s1) of
+// the contraction.
 struct Mx4Tile {
-  int g, nb, p0, n_valid, sg0, sg1;
+  int g, nb, p0, n_valid, s0, s1;
   int64_t tb;  // scale tile of the token tile
 };
 
@@ -256,19 +260,18 @@ __device__ __forceinline__ void store_outputs(const float (&o)[W], void* out, in
   }
 }
 
-template <int MODE, bool F4, int CL, int BN, int STAGES, int KG, int EG, bool SPLIT>
-__global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, KG, EG, SPLIT>::THREADS, 1)
+template <int MODE, bool F4, int CL, int BN, int STAGES, int EG, bool SPLIT>
+__global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, EG, SPLIT>::THREADS, 1)
     mx4_gemm_kernel(const __grid_constant__ Mx4Args args) {
   pdl_trigger();
-  using C = Mx4Cfg<MODE, F4, CL, BN, STAGES, KG, EG, SPLIT>;
+  using C = Mx4Cfg<MODE, F4, CL, BN, STAGES, EG, SPLIT>;
   constexpr bool PAIR = CL == 2;
   constexpr bool GROUPED = MODE != kLinearMx4;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   uint8_t* stages = smem;
-  uint8_t* sfs = stages + (size_t)STAGES * C::STAGE_BYTES;
-  float* epi = reinterpret_cast<float*>(sfs + (size_t)C::SF_STAGES * C::SF_BYTES);
+  float* epi = reinterpret_cast<float*>(stages + (size_t)STAGES * C::STAGE_BYTES);
   uint64_t* bars = reinterpret_cast<uint64_t*>(epi + C::EPI_FLOATS);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + C::NBARS);
   volatile int* epi_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
@@ -289,13 +292,11 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, KG, EG, SPLIT
   auto bar = [&](int i) { return bars_base + 8u * (uint32_t)i; };
   auto full_bar = [&](int s) { return bar(s); };
   auto empty_bar = [&](int s) { return bar(STAGES + s); };
-  auto sffull_bar = [&](int s) { return bar(2 * STAGES + s); };
-  auto sfempty_bar = [&](int s) { return bar(2 * STAGES + C::SF_STAGES + s); };
-  constexpr int B0 = 2 * STAGES + 2 * C::SF_STAGES;
+  constexpr int B0 = 2 * STAGES;
   auto tfull_bar = [&](int a) { return bar(B0 + a); };
   auto tempty_bar = [&](int a) { return bar(B0 + 2 + a); };
   const uint32_t drain_bar = bar(B0 + 4);
-  const uint32_t stages_base = smem_u32(stages), sfs_base = smem_u32(sfs);
+  const uint32_t stages_base = smem_u32(stages);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < B0; ++s) mbar_init(bar(s), 1);
@@ -361,8 +362,8 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, KG, EG, SPLIT
       m = offs[tl.g + 1] - offs[tl.g];
       t.tb = tl.g == E ? 0 : group_scale_tile(offs[tl.g], tl.g, BN);
       t.p0 = tl.g == E ? 0 : offs[tl.g];  // the shared group's rows are in token order
-      t.sg0 = 0;
-      t.sg1 = (args.kt[tl.g == E] + KG - 1) / KG;
+      t.s0 = 0;
+      t.s1 = (args.kt[tl.g == E] + C::KT_STAGE - 1) / C::KT_STAGE;
     } else {
       // Token tiles fastest, so that the CTAs at work share weight rows in L2.
       t.g = 0;
@@ -372,10 +373,10 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, KG, EG, SPLIT
       m = args.T;
       t.tb = 0;
       t.p0 = 0;
-      const int sg = (args.kt[0] + KG - 1) / KG;
+      const int n = (args.kt[0] + C::KT_STAGE - 1) / C::KT_STAGE;
       const int rank = SPLIT ? (int)cluster_ctarank() : 0;
-      t.sg0 = rank * sg / splits;  // never empty: splits <= sg
-      t.sg1 = (rank + 1) * sg / splits;
+      t.s0 = rank * n / splits;  // never empty: splits <= n
+      t.s1 = (rank + 1) * n / splits;
     }
     const int tn = token_tile_rows(m, BN, C::N_UNIT);
     t.tb += mt;
@@ -406,7 +407,7 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, KG, EG, SPLIT
     // of L2 a group's share at a time while this unit's are loaded, and the
     // first unit's at once. Decode layer T=64: 261 -> 217 us (see the table).
     constexpr bool PREFETCH = !PAIR && !SPLIT;
-    constexpr uint32_t PF_BYTES = KG * 8192;
+    constexpr uint32_t PF_BYTES = C::KT_STAGE * 8192;
     auto prefetch_codes = [&](int sh, int rt, int part) {
       const int64_t row_block = (int64_t)args.kt[sh] * 8192;
       const int64_t at = (int64_t)rt * row_block + (int64_t)part * PF_BYTES;
@@ -420,17 +421,16 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, KG, EG, SPLIT
     if (PREFETCH && cid < total) {
       const Mx4Tile t = tile_of(cid);
       const int sh = GROUPED && t.g == E ? 1 : 0;
-      for (int i = lane; i < (args.kt[sh] + KG - 1) / KG; i += 32)
-        prefetch_codes(sh, row_block_of(t, sh), i);
+      for (int i = lane; i < t.s1; i += 32) prefetch_codes(sh, row_block_of(t, sh), i);
       __syncwarp();
     }
     // Test hook: the first stage is neither signalled nor loaded, so that the
     // MMA issuer's wait on it runs out.
     const int skip = (args.flags & MOE_FLAG_TEST_SKIP_SIGNAL) != 0 ? 1 : 0;
-    int first = skip * C::KT_STAGE;
-    int s = skip, ss = 0;         // ring positions
-    uint32_t ph = 1, sph = 1;     // and the parities of their empty barriers
-    uint32_t it = (uint32_t)skip, sit = 0;
+    int first = skip;
+    int s = skip;                 // ring position
+    uint32_t ph = 1;              // and the parity of its empty barrier
+    uint32_t it = (uint32_t)skip;
     bool ok = true;
     for (int u = cid; u < total && ok; u += ncl) {
       const Mx4Tile t = tile_of(u);
@@ -442,11 +442,11 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, KG, EG, SPLIT
       const int need = uniform(mma_cols(t) / CL);
       const int bsel = !PAIR || need > C::BOX1 ? 0 : (need > C::BOX2 ? 1 : 2);
       const int box = bsel == 2 ? C::BOX2 : (bsel == 1 ? C::BOX1 : C::B_ROWS);
-      const uint32_t tx = CL * (C::A_TX + box * 128);
+      const uint32_t tx = C::NB * (C::A_TX + box * 128);
       const int b_row = uniform(t.p0) + crank * need;
       const CUtensorMap *mA = &args.tmA[sh], *mB = &args.tmB[sh][bsel];
       const int sa_row = rt * kt, sb_row = uniform((int)t.tb) * kt * C::RA;
-      const int sg0 = uniform(t.sg0), sg1 = uniform(t.sg1);
+      const int s0 = uniform(t.s0), s1 = uniform(t.s1);
       int next_sh = 0, next_rt = 0;
       const bool has_next = PREFETCH && u + ncl < total;
       if (has_next) {
@@ -454,44 +454,37 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, KG, EG, SPLIT
         next_sh = GROUPED && n.g == E ? 1 : 0;
         next_rt = row_block_of(n, next_sh);
       }
-      for (int sg = sg0; sg < sg1; ++sg) {
-        if (!(ok = warp_wait(sfempty_bar(ss), sph, args.status, limit))) break;
-        const int kend = min(kt, (sg + 1) * KG);
+      for (int st = s0 + first; st < s1; ++st) {
+        if (!(ok = warp_wait(empty_bar(s), ph, args.status, limit))) break;
         if (el) {
-          const uint32_t dst = sfs_base + (uint32_t)(ss * C::SF_BYTES);
+          const uint32_t dst = stages_base + (uint32_t)(s * C::STAGE_BYTES);
+          const int ks = st * C::KT_STAGE;
           if constexpr (PAIR) {
-            // Whole boxes: tiles past the matrix are zeros or never copied on.
-            if (leader) mbar_arrive_expect_tx(sffull_bar(ss), (uint32_t)(CL * C::SF_BYTES));
-            load(dst, &args.tmSA[sh], 0, sa_row + sg * KG, 2 * STAGES + ss, pol_w);
-            load(dst + C::SA_BYTES, &args.tmSB[sh], 0, sb_row + sg * KG * C::RA, 2 * STAGES + ss,
-                 pol_t);
+            // Whole boxes of scale tiles: those past the row are not used.
+            if (leader) mbar_arrive_expect_tx(full_bar(s), 2 * (tx + C::SA_BYTES + C::SB_BYTES));
+            load(dst + C::SA_OFF, &args.tmSA[sh], 0, sa_row + ks, s, pol_w);
+            load(dst + C::SB_OFF, &args.tmSB[sh], 0, sb_row + ks * C::RA, s, pol_t);
           } else {
-            const uint32_t n = (uint32_t)(kend - sg * KG) * 512u;
-            mbar_arrive_expect_tx(sffull_bar(ss), n * (1 + C::RA));
-            bulk_load(dst, args.sA[sh] + ((int64_t)sa_row + sg * KG) * 512, n, sffull_bar(ss),
+            const uint32_t n = (uint32_t)min(C::KT_STAGE, kt - ks) * 512u;
+            mbar_arrive_expect_tx(full_bar(s), tx + n * (1 + C::RA));
+            bulk_load(dst + C::SA_OFF, args.sA[sh] + ((int64_t)sa_row + ks) * 512, n, full_bar(s),
                       pol_w);
-            bulk_load(dst + C::SA_BYTES, args.sB[sh] + ((int64_t)sb_row + sg * KG * C::RA) * 512,
-                      n * C::RA, sffull_bar(ss), pol_t);
-            if (has_next) prefetch_codes(next_sh, next_rt, sg);
+            bulk_load(dst + C::SB_OFF, args.sB[sh] + ((int64_t)sb_row + ks * C::RA) * 512,
+                      n * C::RA, full_bar(s), pol_t);
           }
-        }
-        ++sit;
-        if (++ss == C::SF_STAGES) ss = 0, sph ^= 1u;
-        for (int ks = sg * KG + first; ks < kend; ks += C::KT_STAGE) {
-          if (!(ok = warp_wait(empty_bar(s), ph, args.status, limit))) break;
-          if (el) {
-            const uint32_t dst = stages_base + (uint32_t)(s * C::STAGE_BYTES);
-            const int x = F4 ? ks * 64 : ks * 128;  // bytes, or codes spread by the load
-            if (leader) mbar_arrive_expect_tx(full_bar(s), tx);
-            load(dst, mA, x, rt * 128, s, pol_w);
-            load(dst + C::A_BYTES, mB, x, b_row, s, pol_t);
+#pragma unroll
+          for (int b = 0; b < C::NB; ++b) {
+            // Bytes, or codes that the load spreads; zeros past the row's end.
+            const int x = (ks + b * C::KT_BOX) * (F4 ? 64 : 128);
+            load(dst + b * C::A_BOX, mA, x, rt * 128, s, pol_w);
+            load(dst + C::B_OFF + b * C::B_BOX, mB, x, b_row, s, pol_t);
           }
-          ++it;
-          if (++s == STAGES) s = 0, ph ^= 1u;
+          if (has_next) prefetch_codes(next_sh, next_rt, st);
         }
-        first = 0;
-        if (!ok) break;
+        ++it;
+        if (++s == STAGES) s = 0, ph ^= 1u;
       }
+      first = 0;
     }
     if (MODE == kGatedMx4 && PREFETCH && args.next_codes) {
       // The down GEMM's unit cid: the same groups in the same order (no heavy
@@ -523,10 +516,6 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, KG, EG, SPLIT
         if (skip && i == 0) continue;  // never loaded
         mbar_wait(full_bar((int)(i % STAGES)), (i / STAGES) & 1u, nullptr, 20000000ull);
       }
-      const uint32_t m = sit < (uint32_t)C::SF_STAGES ? sit : (uint32_t)C::SF_STAGES;
-      for (uint32_t i = sit - m; i < sit; ++i)
-        mbar_wait(sffull_bar((int)(i % C::SF_STAGES)), (i / C::SF_STAGES) & 1u, nullptr,
-                  20000000ull);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -540,14 +529,14 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, KG, EG, SPLIT
           umma_commit(b);
       };
       // Operand descriptors differ in their start addresses only.
-      const uint64_t dbase = umma_desc_sw128(stages_base), sbase = scale_tile_desc(sfs_base);
-      int s = 0, ss = 0;
-      uint32_t ph = 0, sph = 0, par = 0, lt = 0;
+      const uint64_t dbase = umma_desc_sw128(stages_base), sbase = scale_tile_desc(stages_base);
+      int s = 0;
+      uint32_t ph = 0, lt = 0;
       bool ok = true;
       for (int u = cid; u < total && ok; u += ncl, ++lt) {
         const Mx4Tile t = tile_of(u);
         const int kt = args.kt[GROUPED ? uniform(t.g == E) : 0];
-        const int sg0 = uniform(t.sg0), sg1 = uniform(t.sg1);
+        const int s0 = uniform(t.s0), s1 = uniform(t.s1);
         const uint32_t acc = lt & 1u;
         if (!(ok = warp_wait(tempty_bar(acc), ((lt >> 1) & 1u) ^ 1u, args.status, limit))) break;
         tc_fence_after();
@@ -555,45 +544,41 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, KG, EG, SPLIT
         const uint32_t idesc = idesc_scaled(F4 ? 1 : 5, F4 ? 1 : 0, 128 * CL,
                                             (uint32_t)uniform(mma_cols(t)), 0);
         uint32_t accumulate = 0;
-        for (int sg = sg0; sg < sg1; ++sg) {
-          if (!(ok = warp_wait(sffull_bar(ss), sph, args.status, limit))) break;
-          const int nk = min(KG, kt - sg * KG);
-          for (int i0 = 0; i0 < nk; i0 += C::KT_STAGE) {
-            if (!(ok = warp_wait(full_bar(s), ph, args.status, limit))) break;
-            tc_fence_after();
-            if (el) {
-              const uint32_t sa = sf_cols + par * C::SF_COLS, sb = sa + C::KT_STAGE * 4;
-              const uint64_t sd = sbase + (uint32_t)((ss * C::SF_BYTES + i0 * 512) >> 4);
-              const uint64_t sbd =
-                  sbase + (uint32_t)((ss * C::SF_BYTES + C::SA_BYTES + i0 * C::RA * 512) >> 4);
-              const uint64_t ad = dbase + (uint32_t)((s * C::STAGE_BYTES) >> 4);
-              const uint64_t bd = ad + (C::A_BYTES >> 4);
+        for (int st = s0; st < s1; ++st) {
+          if (!(ok = warp_wait(full_bar(s), ph, args.status, limit))) break;
+          tc_fence_after();
+          const int nk = min(C::KT_STAGE, kt - st * C::KT_STAGE);  // k tiles of this stage
+          if (el) {
+            const uint32_t at = (uint32_t)(s * C::STAGE_BYTES) >> 4;
 #pragma unroll
-              for (int i = 0; i < C::KT_STAGE; ++i)
-                copy_scale_tile<CL>(sa + i * 4, sd + (uint32_t)(i * 32));
+            for (int b = 0; b < C::NB; ++b) {
+              if (b * C::KT_BOX >= nk) break;
+              const uint32_t sa = sf_cols + b * C::SF_COLS, sb = sa + C::KT_BOX * 4;
+              const uint64_t ad = dbase + (at + (b * C::A_BOX >> 4));
+              const uint64_t bd = dbase + (at + ((C::B_OFF + b * C::B_BOX) >> 4));
+              const uint64_t sad = sbase + (at + ((C::SA_OFF + b * C::KT_BOX * 512) >> 4));
+              const uint64_t sbd = sbase + (at + ((C::SB_OFF + b * C::KT_BOX * C::RA * 512) >> 4));
 #pragma unroll
-              for (int i = 0; i < C::KT_STAGE * C::RA; ++i)
+              for (int i = 0; i < C::KT_BOX; ++i)
+                copy_scale_tile<CL>(sa + i * 4, sad + (uint32_t)(i * 32));
+#pragma unroll
+              for (int i = 0; i < C::KT_BOX * C::RA; ++i)
                 copy_scale_tile<CL>(sb + i * 4, sbd + (uint32_t)(i * 32));
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                const int kti = F4 ? i >> 1 : 0;             // this MMA's k tile of the stage
-                const uint32_t sf = F4 ? (i & 1) * 2 : i;    // and its first block in the tile
-                if (!F4 || i < 2 || i0 + 1 < nk)             // an odd last k tile: half a stage
+                const int kti = F4 ? i >> 1 : 0;           // this MMA's k tile of the box
+                const uint32_t sf = F4 ? (i & 1) * 2 : i;  // and its first block in the tile
+                if (!F4 || i < 2 || b * 2 + 1 < nk)        // an odd last k tile: half a box
                   mma_scaled<CL, F4>(d, ad + (uint32_t)(i * 2), bd + (uint32_t)(i * 2),
                                      idesc | (sf << 4) | (sf << 29), sa + kti * 4,
-                                     sb + kti * 4 * C::RA, i == 0 ? accumulate : 1u);
+                                     sb + kti * 4 * C::RA, b + i == 0 ? accumulate : 1u);
               }
-              commit(empty_bar(s));
             }
-            __syncwarp();
-            accumulate = 1;
-            par ^= 1u;
-            if (++s == STAGES) s = 0, ph ^= 1u;
+            commit(empty_bar(s));
           }
-          if (!ok) break;
-          if (el) commit(sfempty_bar(ss));
           __syncwarp();
-          if (++ss == C::SF_STAGES) ss = 0, sph ^= 1u;
+          accumulate = 1;
+          if (++s == STAGES) s = 0, ph ^= 1u;
         }
         if (!ok) break;
         if (el) commit(tfull_bar(acc));
@@ -810,15 +795,14 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, KG, EG, SPLIT
 }
 
 constexpr int kMaxExperts = 1024;  // the C ABI's limit on E
-constexpr int kScaleGroup = 4;  // k tiles per scale load (KG)
 constexpr int kPairTile = 224;
 
-template <int MODE, bool F4, int CL, int BN, int STAGES, int KG, int EG, bool SPLIT>
+template <int MODE, bool F4, int CL, int BN, int STAGES, int EG, bool SPLIT>
 cudaError_t launch_variant(const Mx4Args& a, int num_sms, size_t units, int splits,
                            cudaStream_t st) {
-  using C = Mx4Cfg<MODE, F4, CL, BN, STAGES, KG, EG, SPLIT>;
+  using C = Mx4Cfg<MODE, F4, CL, BN, STAGES, EG, SPLIT>;
   static_assert(CL == 1 || CL == 2, "single CTAs or pairs");
-  auto fn = mx4_gemm_kernel<MODE, F4, CL, BN, STAGES, KG, EG, SPLIT>;
+  auto fn = mx4_gemm_kernel<MODE, F4, CL, BN, STAGES, EG, SPLIT>;
   cudaError_t e = ensure_smem_attr((const void*)fn, C::smem_bytes(kMaxExperts));
   if (e != cudaSuccess) return e;
   if (units == 0) return cudaSuccess;
@@ -829,25 +813,25 @@ cudaError_t launch_variant(const Mx4Args& a, int num_sms, size_t units, int spli
                         st, (unsigned)cluster, a);
 }
 
-// Token tiles: 32 or 64 rows on single CTAs (9 stages of 20 KB, 7 of 24 KB), 224
-// rows on pairs (5 or 6 stages of 30 KB; two accumulators of 224 columns and
-// the scales fill tensor memory).
+// Token tiles: 32 or 64 rows on single CTAs (4 stages of 42 to 52 KB), 224 rows
+// on pairs (3 stages of 63 or 66 KB; two accumulators of 224 columns and the
+// scales fill tensor memory). One epilogue group where shared memory has no
+// room for two.
 template <int MODE, bool F4>
 cudaError_t launch_mx4(const Mx4Args& a, const Mx4Tiling& t, int num_sms, size_t units, int splits,
                        cudaStream_t st) {
-  constexpr int KG = kScaleGroup;
   if (t.pairs)
-    return launch_variant<MODE, F4, 2, kPairTile, MODE == kDownMx4 ? 6 : 5, KG, 2, false>(
+    return launch_variant<MODE, F4, 2, kPairTile, 3, MODE == kGatedMx4 || F4 ? 1 : 2, false>(
         a, num_sms, units, 1, st);
   if constexpr (MODE == kLinearMx4) {
     if (splits > 1)
       return t.rows == 32
-                 ? launch_variant<MODE, F4, 1, 32, 9, KG, 1, true>(a, num_sms, units, splits, st)
-                 : launch_variant<MODE, F4, 1, 64, 7, KG, 1, true>(a, num_sms, units, splits, st);
+                 ? launch_variant<MODE, F4, 1, 32, 4, 1, true>(a, num_sms, units, splits, st)
+                 : launch_variant<MODE, F4, 1, 64, 4, 1, true>(a, num_sms, units, splits, st);
     if (t.rows == 64)
-      return launch_variant<MODE, F4, 1, 64, 7, KG, 1, false>(a, num_sms, units, 1, st);
+      return launch_variant<MODE, F4, 1, 64, 4, 1, false>(a, num_sms, units, 1, st);
   }
-  return launch_variant<MODE, F4, 1, 32, 9, KG, 1, false>(a, num_sms, units, 1, st);
+  return launch_variant<MODE, F4, 1, 32, 4, 1, false>(a, num_sms, units, 1, st);
 }
 
 struct TokenMaps {
@@ -863,11 +847,11 @@ bool set_tokens(Mx4Args& a, int i, const TokenMaps& t, const Mx4Tiling& tl) {
   const uint64_t cols = (uint64_t)t.kt * (F4 ? 64 : 128);
   a.sB[i] = t.s;
   if (!tl.pairs) return make_tma_map(&a.tmB[i][0], t.q, MOE_DTYPE_E4M3, t.rows, cols, tl.rows);
-  using C = Mx4Cfg<kDownMx4, F4, 2, kPairTile, 4, kScaleGroup, 1, false>;
+  using C = Mx4Cfg<kDownMx4, F4, 2, kPairTile, 3, 1, false>;
   return make_tma_map(&a.tmB[i][0], t.q, MOE_DTYPE_E4M3, t.rows, cols, C::B_ROWS) &&
          make_tma_map(&a.tmB[i][1], t.q, MOE_DTYPE_E4M3, t.rows, cols, C::BOX1) &&
          make_tma_map(&a.tmB[i][2], t.q, MOE_DTYPE_E4M3, t.rows, cols, C::BOX2) &&
-         make_scale_tile_map(&a.tmSB[i], t.s, t.tiles * t.kt * C::RA, kScaleGroup * C::RA);
+         make_scale_tile_map(&a.tmSB[i], t.s, t.tiles * t.kt * C::RA, C::KT_STAGE * C::RA);
 }
 
 template <bool F4>
@@ -880,7 +864,7 @@ bool set_weights(Mx4Args& a, int i, const uint8_t* q, const uint8_t* s, uint64_t
   const bool ok = F4 ? make_tma_map(&a.tmA[i], q, MOE_DTYPE_E4M3, rows, (uint64_t)kt * 64, 128)
                      : make_spread_code_map(&a.tmA[i], q, rows, (uint64_t)kt * 128, 128);
   return ok &&
-         (!tl.pairs || make_scale_tile_map(&a.tmSA[i], s, (rows + 127) / 128 * kt, kScaleGroup));
+         (!tl.pairs || make_scale_tile_map(&a.tmSA[i], s, (rows + 127) / 128 * kt, F4 ? 4 : 2));
 }
 
 }  // namespace
@@ -968,7 +952,7 @@ cudaError_t launch_mx4_down_gemm(const GemmProblem& p, const Mx4Weights& w, cons
 
 // Tiling and clusters over K of a dense product.
 Mx4LinearPlan mx4_linear_plan(int64_t T, int64_t N, int64_t K, int num_sms) {
-  const int64_t sg = (mxfp4_k_tiles(K) + kScaleGroup - 1) / kScaleGroup;
+  const int64_t kt = mxfp4_k_tiles(K);
   const int64_t blocks = (N + 127) / 128;
   // Pairs when they fill at least half of the GPU.
   const int64_t pair_units = (blocks + 1) / 2 * ((T + kPairTile - 1) / kPairTile);
@@ -976,9 +960,9 @@ Mx4LinearPlan mx4_linear_plan(int64_t T, int64_t N, int64_t K, int num_sms) {
   const int rows = T <= 32 ? 32 : 64;
   const int64_t units = blocks * ((T + rows - 1) / rows);
   // As many CTAs per tile as still fit the GPU at once and leave each at least
-  // two scale groups (1024 of K).
+  // 1024 of K (two to four stages).
   int splits = 1;
-  while (splits < 8 && units * splits * 2 <= num_sms && sg >= 4 * splits) splits *= 2;
+  while (splits < 8 && units * splits * 2 <= num_sms && kt >= 16 * splits) splits *= 2;
   return {{false, rows, 16, 1}, splits};
 }
 
