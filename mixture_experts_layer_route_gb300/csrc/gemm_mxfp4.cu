@@ -176,9 +176,25 @@ __device__ __forceinline__ bool elect_lane() {
 // be uniform at compile time, and so is control flow that depends on it.
 __device__ __forceinline__ int uniform(int v) { return __reduce_max_sync(0xffffffffu, v); }
 
-// mbar_wait by a whole warp, with one answer for all of its lanes.
+// A look at a barrier's phase that never suspends the thread.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// mbar_wait by a whole warp, with one answer for all of its lanes. peeked: what
+// mbar_test said earlier, so that the usual case (the phase is complete) does
+// not pay the barrier's latency here.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int* status,
-                                          uint64_t limit_ns) {
+                                          uint64_t limit_ns, bool peeked = false) {
+  if (__all_sync(0xffffffffu, peeked)) return true;
   if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   const uint64_t t0 = globaltimer_ns();
   for (uint32_t it = 1;; ++it) {
@@ -196,7 +212,7 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int* st
 // the contraction.
 struct Mx4Tile {
   int g, nb, p0, n_valid, s0, s1;
-  int64_t tb;  // scale tile of the token tile
+  int tb;  // scale tile of the token tile
 };
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
@@ -350,7 +366,7 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, EG, SPLIT>::T
     lin_mt = (args.T + BN - 1) / BN;
     total = lin_nb * lin_mt;
   }
-  auto tile_of = [&](int u) {
+  auto compute_tile = [&](int u) {
     Mx4Tile t;
     int m, mt;
     if constexpr (GROUPED) {
@@ -360,7 +376,7 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, EG, SPLIT>::T
       t.nb = tl.nb * CL + crank;
       mt = tl.mt;
       m = offs[tl.g + 1] - offs[tl.g];
-      t.tb = tl.g == E ? 0 : group_scale_tile(offs[tl.g], tl.g, BN);
+      t.tb = tl.g == E ? 0 : (int)group_scale_tile(offs[tl.g], tl.g, BN);
       t.p0 = tl.g == E ? 0 : offs[tl.g];  // the shared group's rows are in token order
       t.s0 = 0;
       t.s1 = (args.kt[tl.g == E] + C::KT_STAGE - 1) / C::KT_STAGE;
@@ -384,6 +400,28 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, EG, SPLIT>::T
     t.n_valid = min(tn, m - mt * tn);
     return t;
   };
+  // The tile of this CTA's unit number lt (unit cid + lt ncl). A warp computes 32
+  // units at a time, one a lane (the searches and divisions take ~600 cycles),
+  // and hands each out as a warp-uniform value.
+  Mx4Tile mine = {};
+  auto tile_at = [&](int lt) {
+    if ((lt & 31) == 0) {
+      const int64_t u = cid + (int64_t)(lt + lane) * ncl;
+      if (u < total) mine = compute_tile((int)u);
+      __syncwarp();
+    }
+    const int src = lt & 31;
+    Mx4Tile t;
+    t.g = uniform(__shfl_sync(0xffffffffu, mine.g, src));
+    t.nb = uniform(__shfl_sync(0xffffffffu, mine.nb, src));
+    t.p0 = uniform(__shfl_sync(0xffffffffu, mine.p0, src));
+    t.n_valid = uniform(__shfl_sync(0xffffffffu, mine.n_valid, src));
+    t.tb = uniform(__shfl_sync(0xffffffffu, mine.tb, src));
+    t.s0 = uniform(__shfl_sync(0xffffffffu, mine.s0, src));
+    t.s1 = uniform(__shfl_sync(0xffffffffu, mine.s1, src));
+    return t;
+  };
+  const int n_units = total > cid ? (total - cid + ncl - 1) / ncl : 0;  // of this CTA
   auto mma_cols = [&](const Mx4Tile& t) {
     return (t.n_valid + C::N_UNIT - 1) / C::N_UNIT * C::N_UNIT;
   };
@@ -418,10 +456,11 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, EG, SPLIT>::T
     auto row_block_of = [&](const Mx4Tile& t, int sh) {
       return (sh || !GROUPED ? 0 : t.g * (args.rows[0] / 128)) + t.nb;
     };
-    if (PREFETCH && cid < total) {
-      const Mx4Tile t = tile_of(cid);
-      const int sh = GROUPED && t.g == E ? 1 : 0;
-      for (int i = lane; i < t.s1; i += 32) prefetch_codes(sh, row_block_of(t, sh), i);
+    Mx4Tile next = {};
+    if (n_units > 0) next = tile_at(0);
+    if (PREFETCH && n_units > 0) {
+      const int sh = GROUPED && next.g == E ? 1 : 0;
+      for (int i = lane; i < next.s1; i += 32) prefetch_codes(sh, row_block_of(next, sh), i);
       __syncwarp();
     }
     // Test hook: the first stage is neither signalled nor loaded, so that the
@@ -432,30 +471,33 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, EG, SPLIT>::T
     uint32_t ph = 1;              // and the parity of its empty barrier
     uint32_t it = (uint32_t)skip;
     bool ok = true;
-    for (int u = cid; u < total && ok; u += ncl) {
-      const Mx4Tile t = tile_of(u);
-      const int sh = GROUPED ? uniform(t.g == E) : 0;
+    bool peek = false;
+    for (int lt = 0; lt < n_units && ok; ++lt) {
+      const Mx4Tile t = next;
+      const int sh = GROUPED && t.g == E ? 1 : 0;
       const int kt = args.kt[sh];
       // The last row block of a pair may lie past the group's rows: it loads
       // what is there (another group's rows, or zeros) and stores nothing.
-      const int rt = uniform(row_block_of(t, sh));
-      const int need = uniform(mma_cols(t) / CL);
+      const int rt = row_block_of(t, sh);
+      const int need = mma_cols(t) / CL;
       const int bsel = !PAIR || need > C::BOX1 ? 0 : (need > C::BOX2 ? 1 : 2);
       const int box = bsel == 2 ? C::BOX2 : (bsel == 1 ? C::BOX1 : C::B_ROWS);
       const uint32_t tx = C::NB * (C::A_TX + box * 128);
-      const int b_row = uniform(t.p0) + crank * need;
+      const int b_row = t.p0 + crank * need;
       const CUtensorMap *mA = &args.tmA[sh], *mB = &args.tmB[sh][bsel];
-      const int sa_row = rt * kt, sb_row = uniform((int)t.tb) * kt * C::RA;
-      const int s0 = uniform(t.s0), s1 = uniform(t.s1);
+      const int sa_row = rt * kt, sb_row = t.tb * kt * C::RA;
+      const int s0 = t.s0, s1 = t.s1;
+      const bool has_next = lt + 1 < n_units;
       int next_sh = 0, next_rt = 0;
-      const bool has_next = PREFETCH && u + ncl < total;
       if (has_next) {
-        const Mx4Tile n = tile_of(u + ncl);
-        next_sh = GROUPED && n.g == E ? 1 : 0;
-        next_rt = row_block_of(n, next_sh);
+        next = tile_at(lt + 1);
+        next_sh = GROUPED && next.g == E ? 1 : 0;
+        next_rt = row_block_of(next, next_sh);
       }
       for (int st = s0 + first; st < s1; ++st) {
-        if (!(ok = warp_wait(empty_bar(s), ph, args.status, limit))) break;
+        if (!(ok = warp_wait(empty_bar(s), ph, args.status, limit, peek))) break;
+        const int sn = s + 1 == STAGES ? 0 : s + 1;
+        peek = mbar_test(empty_bar(sn), sn == 0 ? ph ^ 1u : ph);
         if (el) {
           const uint32_t dst = stages_base + (uint32_t)(s * C::STAGE_BYTES);
           const int ks = st * C::KT_STAGE;
@@ -479,7 +521,7 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, EG, SPLIT>::T
             load(dst + b * C::A_BOX, mA, x, rt * 128, s, pol_w);
             load(dst + C::B_OFF + b * C::B_BOX, mB, x, b_row, s, pol_t);
           }
-          if (has_next) prefetch_codes(next_sh, next_rt, st);
+          if (PREFETCH && has_next) prefetch_codes(next_sh, next_rt, st);
         }
         ++it;
         if (++s == STAGES) s = 0, ph ^= 1u;
@@ -531,22 +573,26 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, EG, SPLIT>::T
       // Operand descriptors differ in their start addresses only.
       const uint64_t dbase = umma_desc_sw128(stages_base), sbase = scale_tile_desc(stages_base);
       int s = 0;
-      uint32_t ph = 0, lt = 0;
-      bool ok = true;
-      for (int u = cid; u < total && ok; u += ncl, ++lt) {
-        const Mx4Tile t = tile_of(u);
-        const int kt = args.kt[GROUPED ? uniform(t.g == E) : 0];
-        const int s0 = uniform(t.s0), s1 = uniform(t.s1);
+      uint32_t ph = 0;
+      bool ok = true, peek = false;
+      Mx4Tile next = {};
+      if (n_units > 0) next = tile_at(0);
+      for (int lt = 0; lt < n_units && ok; ++lt) {
+        const Mx4Tile t = next;
+        const int kt = args.kt[GROUPED && t.g == E ? 1 : 0];
+        const int s0 = t.s0, s1 = t.s1;
         const uint32_t acc = lt & 1u;
         if (!(ok = warp_wait(tempty_bar(acc), ((lt >> 1) & 1u) ^ 1u, args.status, limit))) break;
         tc_fence_after();
         const uint32_t d = tmem_base + acc * BN;
         const uint32_t idesc = idesc_scaled(F4 ? 1 : 5, F4 ? 1 : 0, 128 * CL,
-                                            (uint32_t)uniform(mma_cols(t)), 0);
+                                            (uint32_t)mma_cols(t), 0);
         uint32_t accumulate = 0;
         for (int st = s0; st < s1; ++st) {
-          if (!(ok = warp_wait(full_bar(s), ph, args.status, limit))) break;
+          if (!(ok = warp_wait(full_bar(s), ph, args.status, limit, peek))) break;
           tc_fence_after();
+          const int sn = s + 1 == STAGES ? 0 : s + 1;
+          peek = mbar_test(full_bar(sn), sn == 0 ? ph ^ 1u : ph);
           const int nk = min(C::KT_STAGE, kt - st * C::KT_STAGE);  // k tiles of this stage
           if (el) {
             const uint32_t at = (uint32_t)(s * C::STAGE_BYTES) >> 4;
@@ -583,6 +629,7 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, EG, SPLIT>::T
         if (!ok) break;
         if (el) commit(tfull_bar(acc));
         __syncwarp();
+        if (lt + 1 < n_units) next = tile_at(lt + 1);
       }
       if (el) {
         if constexpr (PAIR)
@@ -603,9 +650,8 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, EG, SPLIT>::T
     int32_t* yrow = reinterpret_cast<int32_t*>(epi);
     float* wt = epi + BN;
     float* stage = epi + 2 * BN + eg * 128 * 33;  // [128][33], this group's
-    uint32_t lt = 0;
-    for (int u = cid; u < total; u += ncl, ++lt) {
-      const Mx4Tile t = tile_of(u);
+    for (int lt = 0; lt < n_units; ++lt) {
+      const Mx4Tile t = tile_at(lt);
       const bool shared = GROUPED && t.g == E;
       const uint32_t acc = lt & 1u;
       if (et == 0) *epi_flag = mbar_wait(tfull_bar(acc), (lt >> 1) & 1u, args.status, limit) ? 1 : 0;
@@ -727,7 +773,7 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, EG, SPLIT>::T
               // Features 64 nb: k tile nb / 2, blocks 0,1 or 2,3 of it.
               if (fg == 0)
                 *reinterpret_cast<uint16_t*>(
-                    osc + ((t.tb * kt_out + (t.nb >> 1)) * C::RA + (j >> 7)) * 512 +
+                    osc + (((int64_t)t.tb * kt_out + (t.nb >> 1)) * C::RA + (j >> 7)) * 512 +
                     mxfp4_scale_word((uint32_t)(j & 127)) + (t.nb & 1) * 2) =
                     (uint16_t)(bytes[0] | (bytes[1] << 8));
             }
@@ -767,7 +813,7 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, EG, SPLIT>::T
   if constexpr (SPLIT) {
     // Each CTA adds its share of the tile's outputs over the cluster's partial
     // sums, in the order of K.
-    const Mx4Tile t = tile_of(cid);
+    const Mx4Tile t = compute_tile(cid);
     const int quads = t.n_valid * 32;  // 4 rows of one column each
     const int per = (quads + splits - 1) / splits;
     const int q0 = (int)cluster_ctarank() * per, q1 = min(quads, q0 + per);
