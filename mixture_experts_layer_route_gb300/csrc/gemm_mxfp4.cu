@@ -59,12 +59,6 @@ struct Mx4Args {
   // and the scale tiles as plain addresses (contiguous copies).
   CUtensorMap tmA[2], tmB[2][3], tmSA[2], tmSB[2];
   const uint8_t *sA[2], *sB[2];
-  const uint8_t* codes[2];    // the weights' codes, for L2 prefetches
-  int64_t code_bytes[2];
-  // GATED on single CTAs: the down GEMM's routed weights and their row blocks
-  // per expert, whose first units the CTAs ask L2 for at their end.
-  const uint8_t* next_codes;
-  int next_blocks, next_kt;
   const int32_t* offsets;     // [E+2] (GATED, DOWN)
   const int32_t* gather_idx;  // [T*k] (DOWN)
   const float* topk_w;        // [T*k] (DOWN)
@@ -429,6 +423,10 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, EG, SPLIT>::T
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     const bool el = elect_lane();
+    // Weights that one CTA reads once go past L2 (decode layer T=64: 222 us,
+    // 235 us with evict_normal; asking L2 for a later stage's or the next
+    // unit's codes ahead cost 7% to 17%: the extra lines push out others before
+    // they are read). Pairs of different token tiles share them.
     const uint64_t pol_w = PAIR ? l2_policy_evict_normal() : l2_policy_evict_first();
     const uint64_t pol_t = l2_policy_evict_last();
     // A pair's loads all count on the leader's barriers.
@@ -439,30 +437,11 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, EG, SPLIT>::T
       else
         tma_load_2d(dst, m, x, y, bar(b), pol);
     };
-    // L2 prefetches (single CTAs): a unit's codes are one contiguous range
-    // (128 whole rows). The ring holds 8 KB of codes a stage, too little in
-    // flight to cover HBM's latency; the next unit's codes are therefore asked
-    // of L2 a group's share at a time while this unit's are loaded, and the
-    // first unit's at once. Decode layer T=64: 261 -> 217 us (see the table).
-    constexpr bool PREFETCH = !PAIR && !SPLIT;
-    constexpr uint32_t PF_BYTES = C::KT_STAGE * 8192;
-    auto prefetch_codes = [&](int sh, int rt, int part) {
-      const int64_t row_block = (int64_t)args.kt[sh] * 8192;
-      const int64_t at = (int64_t)rt * row_block + (int64_t)part * PF_BYTES;
-      const int64_t end = min((int64_t)(rt + 1) * row_block, args.code_bytes[sh]);
-      if (at < end)
-        prefetch_l2_bulk(args.codes[sh] + at, (uint32_t)min((int64_t)PF_BYTES, end - at));
-    };
     auto row_block_of = [&](const Mx4Tile& t, int sh) {
       return (sh || !GROUPED ? 0 : t.g * (args.rows[0] / 128)) + t.nb;
     };
     Mx4Tile next = {};
     if (n_units > 0) next = tile_at(0);
-    if (PREFETCH && n_units > 0) {
-      const int sh = GROUPED && next.g == E ? 1 : 0;
-      for (int i = lane; i < next.s1; i += 32) prefetch_codes(sh, row_block_of(next, sh), i);
-      __syncwarp();
-    }
     // Test hook: the first stage is neither signalled nor loaded, so that the
     // MMA issuer's wait on it runs out.
     const int skip = (args.flags & MOE_FLAG_TEST_SKIP_SIGNAL) != 0 ? 1 : 0;
@@ -487,13 +466,7 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, EG, SPLIT>::T
       const CUtensorMap *mA = &args.tmA[sh], *mB = &args.tmB[sh][bsel];
       const int sa_row = rt * kt, sb_row = t.tb * kt * C::RA;
       const int s0 = t.s0, s1 = t.s1;
-      const bool has_next = lt + 1 < n_units;
-      int next_sh = 0, next_rt = 0;
-      if (has_next) {
-        next = tile_at(lt + 1);
-        next_sh = GROUPED && next.g == E ? 1 : 0;
-        next_rt = row_block_of(next, next_sh);
-      }
+      if (lt + 1 < n_units) next = tile_at(lt + 1);
       for (int st = s0 + first; st < s1; ++st) {
         if (!(ok = warp_wait(empty_bar(s), ph, args.status, limit, peek))) break;
         const int sn = s + 1 == STAGES ? 0 : s + 1;
@@ -521,35 +494,11 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, EG, SPLIT>::T
             load(dst + b * C::A_BOX, mA, x, rt * 128, s, pol_w);
             load(dst + C::B_OFF + b * C::B_BOX, mB, x, b_row, s, pol_t);
           }
-          if (PREFETCH && has_next) prefetch_codes(next_sh, next_rt, st);
         }
         ++it;
         if (++s == STAGES) s = 0, ph ^= 1u;
       }
       first = 0;
-    }
-    if (MODE == kGatedMx4 && PREFETCH && args.next_codes) {
-      // The down GEMM's unit cid: the same groups in the same order (no heavy
-      // ones), next_blocks row blocks each instead of rows / 128.
-      const int nf = args.rows[0] / 128;
-      int lo = 0, hi = ngroups;
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if ((int64_t)prefix[mid] / nf * args.next_blocks <= cid) lo = mid;
-        else hi = mid;
-      }
-      if (ngroups > 0 && heavy_units == 0) {
-        const int g = order[lo];
-        const int mtiles = (offs[g + 1] - offs[g] + BN - 1) / BN;
-        const int nb = (cid - prefix[lo] / nf * args.next_blocks) / mtiles;
-        if (g < E && nb < args.next_blocks) {
-          const int64_t bytes = (int64_t)args.next_kt * 8192;
-          const uint8_t* p = args.next_codes + ((int64_t)g * args.next_blocks + nb) * bytes;
-          for (int64_t o = (int64_t)lane * 16384; o < bytes; o += 32 * 16384)
-            prefetch_l2_bulk(p + o, (uint32_t)min((int64_t)16384, bytes - o));
-        }
-      }
-      __syncwarp();
     }
     // Let the last loads land before the CTA (pair) can exit.
     if (el && leader) {
@@ -859,7 +808,7 @@ cudaError_t launch_variant(const Mx4Args& a, int num_sms, size_t units, int spli
                         st, (unsigned)cluster, a);
 }
 
-// Token tiles: 32 or 64 rows on single CTAs (4 stages of 42 to 52 KB), 224 rows
+// Token tiles: 32 or 64 rows on single CTAs (4 or 5 stages of 42 to 52 KB), 224 rows
 // on pairs (3 stages of 63 or 66 KB; two accumulators of 224 columns and the
 // scales fill tensor memory). One epilogue group where shared memory has no
 // room for two.
@@ -877,7 +826,8 @@ cudaError_t launch_mx4(const Mx4Args& a, const Mx4Tiling& t, int num_sms, size_t
     if (t.rows == 64)
       return launch_variant<MODE, F4, 1, 64, 4, 1, false>(a, num_sms, units, 1, st);
   }
-  return launch_variant<MODE, F4, 1, 32, 4, 1, false>(a, num_sms, units, 1, st);
+  return launch_variant<MODE, F4, 1, 32, MODE == kDownMx4 ? 5 : 4, 1, false>(a, num_sms, units, 1,
+                                                                             st);
 }
 
 struct TokenMaps {
@@ -905,8 +855,6 @@ bool set_weights(Mx4Args& a, int i, const uint8_t* q, const uint8_t* s, uint64_t
                  const Mx4Tiling& tl) {
   const int kt = a.kt[i];
   a.sA[i] = s;
-  a.codes[i] = q;
-  a.code_bytes[i] = (int64_t)rows * kt * 64;
   const bool ok = F4 ? make_tma_map(&a.tmA[i], q, MOE_DTYPE_E4M3, rows, (uint64_t)kt * 64, 128)
                      : make_spread_code_map(&a.tmA[i], q, rows, (uint64_t)kt * 128, 128);
   return ok &&
@@ -956,11 +904,6 @@ cudaError_t launch_grouped(const GemmProblem& p, const Mx4Weights& w, const Mx4T
     a.tmSA[1] = a.tmSA[0];
     a.tmSB[1] = a.tmSB[0];
     for (int i = 0; i < 3; ++i) a.tmB[1][i] = a.tmB[0][i];
-  }
-  if (GATED && !has_s) {
-    a.next_codes = w.down;
-    a.next_blocks = p.H / 128;
-    a.next_kt = p.I / 128;
   }
   a.offsets = offsets;
   a.gather_idx = gather_idx;
