@@ -36,7 +36,7 @@
 //
 // Warp roles: warp 0 TMA producer, warp 1 MMA issuer (one thread) and owner of
 // the tensor memory, the others epilogue (four per group, one 32-lane quarter
-// each; groups take alternate 32-column chunks). Two accumulators let a unit's
+// each; groups take alternate 16-column chunks). Two accumulators let a unit's
 // epilogue run under the next unit's main loop. CL = 2: CTA pairs
 // (cta_group::2), each CTA with its own 128 weight rows and half of the token
 // rows, the leader issuing for both (see grouped_gemm.cuh). Every wait is
@@ -60,11 +60,9 @@ struct Mx4Args {
   CUtensorMap tmA[2], tmB[2][3], tmSA[2], tmSB[2];
   const uint8_t *sA[2], *sB[2];
   const int32_t* offsets;     // [E+2] (GATED, DOWN)
-  const int32_t* gather_idx;  // [T*k] (DOWN)
-  const float* topk_w;        // [T*k] (DOWN)
-  // GATED: h codes by position; DOWN: Y fp32 [T][KP][H]; LINEAR: y [T][N].
+  // GATED: h codes by position; DOWN: slot rows (Mx4Slots); LINEAR: y [T][N].
   void* out;
-  uint8_t* out_s;             // GATED: scale tiles of h
+  uint8_t* out_s;             // GATED: scale tiles of h; DOWN: the slots' scales
   void* out_shared;           // GATED: shared h codes by token, and their scale tiles
   uint8_t* out_shared_s;
   int* status;
@@ -102,7 +100,8 @@ struct Mx4Cfg {
   static constexpr int EPI_GROUPS = EG;
   static constexpr int EPI_THREADS = 128 * EG;
   static constexpr int THREADS = 64 + EPI_THREADS;
-  static constexpr int EPI_FLOATS = (MODE == kDownMx4 ? 0 : EG * 128 * 33) + 2 * BN;
+  static constexpr int EPI_BUF = 16 * 36;  // floats per epilogue warp: 16 tokens x 32 rows, padded
+  static constexpr int EPI_FLOATS = EG * 4 * EPI_BUF;
   // full, empty [STAGES]; tfull, tempty [2]; drain
   static constexpr int NBARS = 2 * STAGES + 5;
   static_assert(!SPLIT || (MODE == kLinearMx4 && CL == 1), "clusters over K: dense, single CTAs");
@@ -231,6 +230,32 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
                : "r"(addr)
                : "memory");
   return v;
+}
+
+// Each thread of the warp reads 16 consecutive fp32 columns of its own
+// tensor-memory lane.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// Bits of the largest magnitude of the 32 values that four lanes hold 8 each of.
+__device__ __forceinline__ uint32_t amax_of_four(const float (&v)[8]) {
+  uint32_t a = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) a = max(a, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+  a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
+  return max(a, __shfl_xor_sync(0xffffffffu, a, 2));
 }
 
 // The epilogue's stores of 8 (or 4) consecutive outputs of a row from column n0.
@@ -594,74 +619,18 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, EG, SPLIT>::T
     const int q = warp & 3;               // tensor-memory lane quarter
     const int eg = (warp - 2) >> 2;       // chunk group
     const int et = threadIdx.x - 64;      // 0..EPI_THREADS-1
-    const int gt = et & 127;              // thread of the group
     const uint32_t lane_base = (uint32_t)(q * 32) << 16;
-    int32_t* yrow = reinterpret_cast<int32_t*>(epi);
-    float* wt = epi + BN;
-    float* stage = epi + 2 * BN + eg * 128 * 33;  // [128][33], this group's
     for (int lt = 0; lt < n_units; ++lt) {
       const Mx4Tile t = tile_at(lt);
       const bool shared = GROUPED && t.g == E;
       const uint32_t acc = lt & 1u;
       if (et == 0) *epi_flag = mbar_wait(tfull_bar(acc), (lt >> 1) & 1u, args.status, limit) ? 1 : 0;
-      if constexpr (MODE == kDownMx4) {
-        // Destination row in Y and gate weight of each column.
-        for (int j = et; j < t.n_valid; j += C::EPI_THREADS) {
-          int row;
-          float wv;
-          if (shared) {
-            row = (t.p0 + j) * args.KP + args.k;
-            wv = 1.0f;
-          } else {
-            const int s = args.gather_idx[t.p0 + j];
-            if ((unsigned)s < (unsigned)(args.T * args.k)) {
-              const int tok = s / args.k;
-              row = tok * args.KP + (s - tok * args.k);
-              wv = args.topk_w[s];
-            } else {  // device check: reported; the column goes to row 0 as zeros
-              set_status(args.status, MOE_ERR_DEVICE_CHECK);
-              row = 0;
-              wv = 0.f;
-            }
-          }
-          yrow[j] = row;
-          wt[j] = wv;
-        }
-      }
       named_barrier_sync(1, C::EPI_THREADS);
       if (!*epi_flag) break;  // every epilogue thread sees the same flag
       tc_fence_after();
       const uint32_t t_acc = tmem_base + lane_base + acc * BN;
       const bool live = t.nb * 128 < args.rows[shared];  // a pair's block past the last one
-      if constexpr (MODE == kDownMx4) {
-        // Thread = output feature; a warp stores 32 consecutive floats of a
-        // token's slot row per column.
-        const size_t H = (size_t)args.rows[0];
-        float* Yc = reinterpret_cast<float*>(args.out) + (size_t)t.nb * 128 + q * 32 + lane;
-        const int4* yrow4 = reinterpret_cast<const int4*>(yrow);
-        const float4* wt4 = reinterpret_cast<const float4*>(wt);
-        for (int c0 = 32 * eg; live && c0 < t.n_valid; c0 += 32 * EG) {
-          float v[32];
-          tmem_ld32(t_acc + c0, v);
-          const int nj = min(32, t.n_valid - c0);
-#pragma unroll
-          for (int i4 = 0; i4 < 8; ++i4) {
-            const int4 r = yrow4[(c0 >> 2) + i4];
-            const float4 wv = wt4[(c0 >> 2) + i4];
-            const int i = 4 * i4;
-            if (i + 3 < nj) {
-              Yc[(size_t)r.x * H] = wv.x * v[i];
-              Yc[(size_t)r.y * H] = wv.y * v[i + 1];
-              Yc[(size_t)r.z * H] = wv.z * v[i + 2];
-              Yc[(size_t)r.w * H] = wv.w * v[i + 3];
-            } else {
-              if (i < nj) Yc[(size_t)r.x * H] = wv.x * v[i];
-              if (i + 1 < nj) Yc[(size_t)r.y * H] = wv.y * v[i + 1];
-              if (i + 2 < nj) Yc[(size_t)r.z * H] = wv.z * v[i + 2];
-            }
-          }
-        }
-      } else if constexpr (SPLIT) {
+      if constexpr (SPLIT) {
         // Partial sums to shared memory ([column][row], over the drained ring);
         // the cluster adds them below.
         float* part = reinterpret_cast<float*>(stages);
@@ -672,74 +641,87 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, EG, SPLIT>::T
           for (int i = 0; i < 32; ++i) part[(c0 + i) * 128 + q * 32 + lane] = v[i];
         }
       } else {
-        // 32 columns at a time through shared memory: lanes hold weight rows,
-        // and both epilogues want several rows of one token in a thread.
-        // Thread: token column jj, rows 8 fg + 0..7 of each 32-row block (a
-        // warp's eight tokens and four row groups fall on 32 distinct banks).
-        const int jj = gt >> 2, fg = gt & 3;
-        for (int c0 = 32 * eg; live && c0 < t.n_valid; c0 += 32 * EG) {
-          float v[32];
-          tmem_ld32(t_acc + c0, v);
+        // 16 columns (tokens) at a time. A warp holds 32 weight rows, one a lane,
+        // of each; the outputs want consecutive rows of one token in a thread.
+        // Every warp turns its 32 x 16 block around in a buffer of its own, at
+        // most two warps meeting in a barrier. Thread: 8 rows (part) of token
+        // lane / 4, so that 16-byte stores cover 64 consecutive bytes a token.
+        const int tok = lane >> 2, part = lane & 3;
+        float* bufs = epi + eg * 4 * C::EPI_BUF;
+        float* mine_buf = bufs + q * C::EPI_BUF;
+        for (int c0 = 16 * eg; live && c0 < t.n_valid; c0 += 16 * EG) {
+          float v[16];
+          tmem_ld16(t_acc + c0, v);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) stage[(q * 32 + lane) * 33 + i] = v[i];
-          named_barrier_sync(2 + eg, 128);
-          const int j = c0 + jj;
+          for (int i = 0; i < 16; ++i) mine_buf[i * 36 + lane] = v[i];
           if constexpr (MODE == kGatedMx4) {
-            // Rows 0..63 are gate, 64..127 up, of features 64 nb ..; h is
-            // quantized from fp32 per 32 features (the four threads of a token
-            // hold a block).
-            const int kt_out = args.rows[shared] / 256;  // I / 128
-            uint32_t bytes[2];
-            uint2 codes[2];
+            // Rows 0..63 are gate, 64..127 up, of features 64 nb ..: warps q and
+            // q + 2 share 32 features, a block of h, which is quantized from
+            // fp32; each takes 8 of the tokens.
+            const int b = q & 1;
+            named_barrier_sync(2 + eg * 2 + b, 64);
+            const int pt = (q >> 1) * 8 + tok;
+            const float* gb = bufs + b * C::EPI_BUF + pt * 36 + part * 8;
+            const float* ub = gb + 2 * C::EPI_BUF;
+            float hv[8];
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-              float hv[8];
-              uint32_t amax = 0;
+            for (int i4 = 0; i4 < 2; ++i4) {
+              const float4 g4 = reinterpret_cast<const float4*>(gb)[i4];
+              const float4 u4 = reinterpret_cast<const float4*>(ub)[i4];
+              const float g[4] = {g4.x, g4.y, g4.z, g4.w}, u[4] = {u4.x, u4.y, u4.z, u4.w};
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float g = stage[(b * 32 + fg * 8 + i) * 33 + jj];
-                const float up = stage[(64 + b * 32 + fg * 8 + i) * 33 + jj];
+              for (int i = 0; i < 4; ++i)
                 // silu(g) * up; approximate exp and divide (a few ulp of fp32,
                 // far below the E4M3 rounding that follows).
-                hv[i] = __fdividef(g, 1.0f + __expf(-g)) * up;
-                amax = max(amax, __float_as_uint(hv[i]) & 0x7FFFFFFFu);
-              }
-              amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-              amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-              bytes[b] = mx_scale_byte(amax, 8);
-              const float inv = mx_inv_scale(bytes[b]);
-              codes[b] = make_uint2(mx_encode4(mx_scaled(hv[0], inv), mx_scaled(hv[1], inv),
-                                               mx_scaled(hv[2], inv), mx_scaled(hv[3], inv)),
-                                    mx_encode4(mx_scaled(hv[4], inv), mx_scaled(hv[5], inv),
-                                               mx_scaled(hv[6], inv), mx_scaled(hv[7], inv)));
+                hv[i4 * 4 + i] = __fdividef(g[i], 1.0f + __expf(-g[i])) * u[i];
             }
+            const uint32_t byte = mx_scale_byte(amax_of_four(hv), 8);
+            const float inv = mx_inv_scale(byte);
+            const int j = c0 + pt;
             if (j < t.n_valid) {
+              const int kt_out = args.rows[shared] / 256;  // I / 128
               uint8_t* out = reinterpret_cast<uint8_t*>(shared ? args.out_shared : args.out);
               uint8_t* osc = shared ? args.out_shared_s : args.out_s;
-              uint8_t* dst = out + (size_t)(t.p0 + j) * (kt_out * 128) + t.nb * 64 + fg * 8;
-              *reinterpret_cast<uint2*>(dst) = codes[0];
-              *reinterpret_cast<uint2*>(dst + 32) = codes[1];
+              uint2 codes = make_uint2(mx_encode4(hv[0] * inv, hv[1] * inv, hv[2] * inv, hv[3] * inv),
+                                       mx_encode4(hv[4] * inv, hv[5] * inv, hv[6] * inv, hv[7] * inv));
+              if (byte == 255u) codes = make_uint2(0, 0);  // a NaN block
+              *reinterpret_cast<uint2*>(out + (size_t)(t.p0 + j) * (kt_out * 128) + t.nb * 64 +
+                                        b * 32 + part * 8) = codes;
               // Features 64 nb: k tile nb / 2, blocks 0,1 or 2,3 of it.
-              if (fg == 0)
-                *reinterpret_cast<uint16_t*>(
-                    osc + (((int64_t)t.tb * kt_out + (t.nb >> 1)) * C::RA + (j >> 7)) * 512 +
-                    mxfp4_scale_word((uint32_t)(j & 127)) + (t.nb & 1) * 2) =
-                    (uint16_t)(bytes[0] | (bytes[1] << 8));
+              if (part == 0)
+                osc[(((int64_t)t.tb * kt_out + (t.nb >> 1)) * C::RA + (j >> 7)) * 512 +
+                    mxfp4_scale_word((uint32_t)(j & 127)) + (t.nb & 1) * 2 + b] = (uint8_t)byte;
             }
+            named_barrier_sync(2 + eg * 2 + b, 64);
           } else {
-            if (j < t.n_valid) {
+            __syncwarp();
 #pragma unroll
-              for (int b = 0; b < 4; ++b) {
-                float o[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) o[i] = stage[(b * 32 + fg * 8 + i) * 33 + jj];
+            for (int i = 0; i < 2; ++i) {
+              const int pt = i * 8 + tok, j = c0 + pt;
+              const float4* src = reinterpret_cast<const float4*>(mine_buf + pt * 36 + part * 8);
+              const float4 lo = src[0], hi = src[1];
+              const float o[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+              if constexpr (MODE == kDownMx4) {
+                // The warp's 32 features are a block of the position's slot row.
+                const uint32_t byte = slot_scale_byte(amax_of_four(o));
+                const float inv = mx_inv_scale(byte);
+                if (j < t.n_valid) {
+                  const int64_t at = ((int64_t)(shared ? args.T * args.k : 0) + t.p0 + j) *
+                                         (args.rows[0] / 32) +
+                                     t.nb * 4 + q;
+                  reinterpret_cast<uint4*>(args.out)[at * 4 + part] =
+                      make_uint4(slot_pair(o[0], o[1], inv), slot_pair(o[2], o[3], inv),
+                                 slot_pair(o[4], o[5], inv), slot_pair(o[6], o[7], inv));
+                  if (part == 0) args.out_s[at] = (uint8_t)byte;
+                }
+              } else if (j < t.n_valid) {
                 store_outputs(o, args.out, (int64_t)(t.p0 + j) * args.ld_out,
-                              t.nb * 128 + b * 32 + fg * 8, args.rows[0], args.out_f32 != 0,
+                              t.nb * 128 + q * 32 + part * 8, args.rows[0], args.out_f32 != 0,
                               args.vec_out != 0);
               }
             }
+            __syncwarp();
           }
-          named_barrier_sync(2 + eg, 128);
         }
       }
       tc_fence_before();
@@ -808,16 +790,14 @@ cudaError_t launch_variant(const Mx4Args& a, int num_sms, size_t units, int spli
                         st, (unsigned)cluster, a);
 }
 
-// Token tiles: 32 or 64 rows on single CTAs (4 or 5 stages of 42 to 52 KB), 224 rows
+// Token tiles: 32 or 64 rows on single CTAs (4 stages of 42 to 52 KB), 224 rows
 // on pairs (3 stages of 63 or 66 KB; two accumulators of 224 columns and the
-// scales fill tensor memory). One epilogue group where shared memory has no
-// room for two.
+// scales fill tensor memory; two epilogue groups).
 template <int MODE, bool F4>
 cudaError_t launch_mx4(const Mx4Args& a, const Mx4Tiling& t, int num_sms, size_t units, int splits,
                        cudaStream_t st) {
   if (t.pairs)
-    return launch_variant<MODE, F4, 2, kPairTile, 3, MODE == kGatedMx4 || F4 ? 1 : 2, false>(
-        a, num_sms, units, 1, st);
+    return launch_variant<MODE, F4, 2, kPairTile, 3, 2, false>(a, num_sms, units, 1, st);
   if constexpr (MODE == kLinearMx4) {
     if (splits > 1)
       return t.rows == 32
@@ -826,8 +806,7 @@ cudaError_t launch_mx4(const Mx4Args& a, const Mx4Tiling& t, int num_sms, size_t
     if (t.rows == 64)
       return launch_variant<MODE, F4, 1, 64, 4, 1, false>(a, num_sms, units, 1, st);
   }
-  return launch_variant<MODE, F4, 1, 32, MODE == kDownMx4 ? 5 : 4, 1, false>(a, num_sms, units, 1,
-                                                                             st);
+  return launch_variant<MODE, F4, 1, 32, 4, 1, false>(a, num_sms, units, 1, st);
 }
 
 struct TokenMaps {
@@ -874,8 +853,8 @@ namespace {
 
 template <int MODE>
 cudaError_t launch_grouped(const GemmProblem& p, const Mx4Weights& w, const Mx4Tokens& x,
-                           const int32_t* offsets, const int32_t* gather_idx, const float* topk_w,
-                           const Mx4Out& out, float* Y, int* status, cudaStream_t st) {
+                           const int32_t* offsets, const Mx4Out& out, int* status,
+                           cudaStream_t st) {
   constexpr bool GATED = MODE == kGatedMx4;
   const bool has_s = p.Is > 0;
   Mx4Args a;
@@ -906,9 +885,7 @@ cudaError_t launch_grouped(const GemmProblem& p, const Mx4Weights& w, const Mx4T
     for (int i = 0; i < 3; ++i) a.tmB[1][i] = a.tmB[0][i];
   }
   a.offsets = offsets;
-  a.gather_idx = gather_idx;
-  a.topk_w = topk_w;
-  a.out = GATED ? (void*)out.routed : (void*)Y;
+  a.out = out.routed;
   a.out_s = out.routed_s;
   a.out_shared = out.shared;
   a.out_shared_s = out.shared_s;
@@ -930,13 +907,14 @@ cudaError_t launch_grouped(const GemmProblem& p, const Mx4Weights& w, const Mx4T
 cudaError_t launch_mx4_swiglu_gemm(const GemmProblem& p, const Mx4Weights& w, const Mx4Tokens& x,
                                    const int32_t* offsets, const Mx4Out& h, int* status,
                                    cudaStream_t st) {
-  return launch_grouped<kGatedMx4>(p, w, x, offsets, nullptr, nullptr, h, nullptr, status, st);
+  return launch_grouped<kGatedMx4>(p, w, x, offsets, h, status, st);
 }
 
 cudaError_t launch_mx4_down_gemm(const GemmProblem& p, const Mx4Weights& w, const Mx4Tokens& h,
-                                 const int32_t* offsets, const int32_t* gather_idx,
-                                 const float* topk_w, float* Y, int* status, cudaStream_t st) {
-  return launch_grouped<kDownMx4>(p, w, h, offsets, gather_idx, topk_w, Mx4Out{}, Y, status, st);
+                                 const int32_t* offsets, const Mx4Slots& y, int* status,
+                                 cudaStream_t st) {
+  const Mx4Out out = {reinterpret_cast<uint8_t*>(y.q), y.s, nullptr, nullptr};
+  return launch_grouped<kDownMx4>(p, w, h, offsets, out, status, st);
 }
 
 // Tiling and clusters over K of a dense product.

@@ -44,6 +44,7 @@ struct Layout {
   // (xq above holds the codes), their expert-ordered copies (xg holds the
   // codes), and the scale rows of h and h_shared (h, hs hold the codes).
   size_t xs, xgs, hsc, hss;
+  size_t ys;  // MXFP4 layers only: the slots' scales (Y holds their int16 codes)
   bool mx_dec;
   // MXFP4 layers: token codes in expert order (xg) with their scale tiles (xgs
   // above), in token order for a shared expert (xq, xs); h and h_shared codes
@@ -155,7 +156,8 @@ Layout layout_of(const moe_problem& p) {
   L.sh = f8 ? take(T * k * 4) : 0;
   L.hsq = f8 && p.I_shared > 0 ? take(T * (size_t)p.I_shared) : 0;
   L.shs = f8 && p.I_shared > 0 ? take(T * 4) : 0;
-  L.Y = take(T * KP * (size_t)p.H * 4);
+  L.Y = take(T * KP * (size_t)p.H * (m4 ? 2 : 4));
+  L.ys = m4 ? take(T * KP * (size_t)(p.H / 32)) : 0;
   // Single-launch decode kernel: per-group counts of finished gate/up units.
   L.units = take((E + 2) * 4);
   // ... and its router partial sums (at most 8 slices of H), for decode-sized
@@ -861,7 +863,7 @@ moe_status moe_forward_mxfp4(const moe_problem* pb, const void* x, const void* W
   int32_t* offs = at<int32_t>(workspace, L.offsets);
   int32_t* gidx = at<int32_t>(workspace, L.gather);
   int32_t* spos = at<int32_t>(workspace, L.slotpos);
-  float* Y = at<float>(workspace, L.Y);
+  const Mx4Slots Y = {at<int16_t>(workspace, L.Y), at<uint8_t>(workspace, L.ys)};
   const Mx4Weights mw = {Wq_gate_up, s_gate_up, Wq_down, s_down,
                          Wsq_gate_up, ss_gate_up, Wsq_down, ss_down};
   uint8_t* xq = has_s ? at<uint8_t>(workspace, L.xq) : nullptr;
@@ -917,12 +919,11 @@ moe_status moe_forward_mxfp4(const moe_problem* pb, const void* x, const void* W
   }
   if (e == cudaSuccess) {
     NvtxRange r("down_gemm");
-    e = launch_mx4_down_gemm(g, mw, ht, offs, gidx, w, Y, status, st);
+    e = launch_mx4_down_gemm(g, mw, ht, offs, Y, status, st);
   }
   if (e == cudaSuccess) {
     NvtxRange r("combine");
-    e = launch_combine(pb->out_f32 ? MOE_DTYPE_F32 : MOE_DTYPE_BF16, Y, g.T, g.H,
-                       g.k + (has_s ? 1 : 0), y, g.num_sms, st);
+    e = launch_mx4_combine(Y, spos, w, g.T, g.k, g.H, has_s, pb->out_f32 != 0, y, status, st);
   }
   return cuda_status(e);
 }
