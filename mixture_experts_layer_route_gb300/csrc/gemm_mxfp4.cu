@@ -41,6 +41,7 @@
 // (cta_group::2), each CTA with its own 128 weight rows and half of the token
 // rows, the leader issuing for both (see grouped_gemm.cuh). Every wait is
 // bounded (status word).
+#include <climits>
 #include <cstring>
 
 #include "grouped_gemm.cuh"
@@ -51,25 +52,34 @@ namespace moe {
 
 namespace {
 
-enum Mx4Mode : int { kGatedMx4 = 0, kDownMx4 = 1, kLinearMx4 = 2 };
+// kExpertsMx4: the gate/up and the down GEMM as two phases of one launch.
+enum Mx4Mode : int { kGatedMx4 = 0, kDownMx4 = 1, kLinearMx4 = 2, kExpertsMx4 = 3 };
 
-struct Mx4Args {
-  // [0] routed, [1] shared group. Pairs: token boxes of B_ROWS, BOX1 and BOX2
-  // rows and maps of the scale tiles; single CTAs: one token box (tmB[.][0]),
-  // and the scale tiles as plain addresses (contiguous copies).
+// The operands and outputs of one GEMM; [0] routed, [1] shared group.
+struct Mx4Phase {
+  // Pairs: token boxes of B_ROWS, BOX1 and BOX2 rows and maps of the scale
+  // tiles; single CTAs: one token box (tmB[.][0]), and the scale tiles as plain
+  // addresses (contiguous copies).
   CUtensorMap tmA[2], tmB[2][3], tmSA[2], tmSB[2];
   const uint8_t *sA[2], *sB[2];
-  const int32_t* offsets;     // [E+2] (GATED, DOWN)
+  int rows[2];                // weight rows per group (GATED: 2 I)
+  int kt[2];                  // k tiles (of 128) of the contraction
   // GATED: h codes by position; DOWN: slot rows (Mx4Slots); LINEAR: y [T][N].
   void* out;
   uint8_t* out_s;             // GATED: scale tiles of h; DOWN: the slots' scales
   void* out_shared;           // GATED: shared h codes by token, and their scale tiles
   uint8_t* out_shared_s;
+};
+
+struct Mx4Args {
+  Mx4Phase ph[2];             // [1]: kExpertsMx4 only (DOWN)
+  const int32_t* offsets;     // [E+2] (grouped modes)
+  int* done;                  // kExpertsMx4: finished gate/up row blocks of every token
+                              // tile (by scale tile; the shared group's after done_shared)
+  int done_shared;
   int* status;
   unsigned long long limit_ns;
   int T, k, E, KP;
-  int rows[2];                // weight rows per group (GATED: 2 I)
-  int kt[2];                  // k tiles (of 128) of the contraction
   unsigned flags;
   // LINEAR
   int64_t ld_out;
@@ -109,7 +119,7 @@ struct Mx4Cfg {
   static_assert(STAGE_BYTES % 1024 == 0 && B_BOX % 1024 == 0, "swizzled boxes start on 1 KB");
 
   static size_t smem_bytes(int E) {
-    return 1024 + (size_t)STAGES * STAGE_BYTES + EPI_FLOATS * 4 + NBARS * 8 + 16 + (MODE == kLinearMx4 ? 0 : 3 * (size_t)(E + 2) * 4);
+    return 1024 + (size_t)STAGES * STAGE_BYTES + EPI_FLOATS * 4 + NBARS * 8 + 32 + (MODE == kLinearMx4 ? 0 : 3 * (size_t)(E + 2) * 4);
   }
 };
 
@@ -204,7 +214,7 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int* st
 // take 2 nb and 2 nb + 1) of group g on one token tile, over stages [s0, s1) of
 // the contraction.
 struct Mx4Tile {
-  int g, nb, p0, n_valid, s0, s1;
+  int phase, g, nb, p0, n_valid, s0, s1;
   int tb;  // scale tile of the token tile
 };
 
@@ -295,21 +305,25 @@ __device__ __forceinline__ void store_outputs(const float (&o)[W], void* out, in
   }
 }
 
-// The unit schedule of build_schedule (grouped_gemm.cuh: the groups with rows,
-// heaviest class first, prefix[i] units before the i-th), built by all threads
-// of the block: one warp takes ~3 us for 128 experts, this 0.7. Chunks of 32
-// groups count their groups and units per class; the counts before each chunk
-// come from all chunks' (at most 33), then every group finds its own place.
-// scratch: 33 * 8 ints of shared memory.
-template <int UNIT_ROWS, int THREADS>
+struct Mx4Schedule {
+  int groups;        // groups with rows
+  int heavy;         // of more than 128 rows: the first ones of the order
+  int shared_at;     // place of the shared group in the order (INT_MAX: none)
+  int shared_tiles;  // and its token tiles
+};
+
+// The order of build_schedule (grouped_gemm.cuh: the groups with rows, heaviest
+// class first), with prefix[i] token tiles before the i-th, built by all threads
+// of the block. Chunks of 32 groups count their groups and tiles per class; the
+// counts before each chunk come from all chunks' (at most 33), then every group
+// finds its own place. scratch: 33 * 8 ints of shared memory.
+template <int THREADS>
 __device__ __forceinline__ void build_schedule_block(const Mx4Args& a, int tile_n, int32_t* offs,
-                                                     int32_t* order, int32_t* prefix, int* n_sched,
-                                                     int* n_heavy, int32_t* scratch) {
+                                                     int32_t* order, int32_t* prefix,
+                                                     Mx4Schedule* out, int32_t* scratch) {
   const int G = a.E + 1, P = a.T * a.k;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int NW = THREADS / 32;
-  const int nf[2] = {(a.rows[0] + UNIT_ROWS - 1) / UNIT_ROWS,
-                     (a.rows[1] + UNIT_ROWS - 1) / UNIT_ROWS};
   // Device check: offsets start at 0, never decrease, stay within the routed
   // positions, and the shared group has 0 or T rows; otherwise no unit runs.
   bool bad = false;
@@ -324,26 +338,25 @@ __device__ __forceinline__ void build_schedule_block(const Mx4Args& a, int tile_
     if (tid == 0) {
       set_status(a.status, MOE_ERR_DEVICE_CHECK);
       prefix[0] = 0;
-      *n_sched = 0;
-      *n_heavy = 0;
+      *out = {0, 0, INT_MAX, 0};
     }
     __syncthreads();
     return;
   }
   const int chunks = (G + 31) / 32;
-  auto group = [&](int c, int& cls, int& units) {
+  auto group = [&](int c, int& cls, int& tiles) {
     const int g = c * 32 + lane;
     const int m = g < G ? offs[g + 1] - offs[g] : 0;
     cls = m <= 0 ? 4 : (m > 256 ? 0 : (m > 128 ? 1 : (m > 32 ? 2 : 3)));
-    units = (m + tile_n - 1) / tile_n * nf[g == a.E];
+    tiles = (m + tile_n - 1) / tile_n;
   };
   for (int c = warp; c < chunks; c += NW) {
-    int cls, units;
-    group(c, cls, units);
+    int cls, tiles;
+    group(c, cls, tiles);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const uint32_t in = __ballot_sync(0xffffffffu, cls == k);
-      const int u = __reduce_add_sync(0xffffffffu, cls == k ? units : 0);
+      const int u = __reduce_add_sync(0xffffffffu, cls == k ? tiles : 0);
       if (lane == 0) {
         scratch[c * 8 + k] = __popc(in);
         scratch[c * 8 + 4 + k] = u;
@@ -352,12 +365,12 @@ __device__ __forceinline__ void build_schedule_block(const Mx4Args& a, int tile_
   }
   __syncthreads();
   for (int c = warp; c < chunks; c += NW) {
-    int cls, units;
-    group(c, cls, units);
-    int first_group = 0, first_unit = 0, groups_all = 0, units_all = 0, heavy = 0;
+    int cls, tiles;
+    group(c, cls, tiles);
+    int first_group = 0, first_tile = 0, groups_all = 0, tiles_all = 0, heavy = 0;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      // Groups and units of class k in the chunks before this one, and in all.
+      // Groups and tiles of class k in the chunks before this one, and in all.
       int gb = 0, ub = 0, ga = 0, ua = 0;
       for (int i = lane; i < chunks; i += 32) {
         const int x = scratch[i * 8 + k], y = scratch[i * 8 + 4 + k];
@@ -368,7 +381,7 @@ __device__ __forceinline__ void build_schedule_block(const Mx4Args& a, int tile_
       gb = __reduce_add_sync(0xffffffffu, gb);
       ub = __reduce_add_sync(0xffffffffu, ub);
       const uint32_t in = __ballot_sync(0xffffffffu, cls == k);
-      int scan = cls == k ? units : 0;
+      int scan = cls == k ? tiles : 0;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xffffffffu, scan, o);
@@ -376,20 +389,24 @@ __device__ __forceinline__ void build_schedule_block(const Mx4Args& a, int tile_
       }
       if (cls == k) {
         first_group = groups_all + gb + __popc(in & ((1u << lane) - 1u));
-        first_unit = units_all + ub + scan - units;
+        first_tile = tiles_all + ub + scan - tiles;
       }
       groups_all += __reduce_add_sync(0xffffffffu, ga);
-      units_all += __reduce_add_sync(0xffffffffu, ua);
-      if (k == 1) heavy = units_all;
+      tiles_all += __reduce_add_sync(0xffffffffu, ua);
+      if (k == 1) heavy = groups_all;
     }
     if (cls < 4) {
       order[first_group] = c * 32 + lane;
-      prefix[first_group] = first_unit;
+      prefix[first_group] = first_tile;
     }
-    if (c == 0 && lane == 0) {
-      prefix[groups_all] = units_all;
-      *n_sched = groups_all;
-      *n_heavy = heavy;
+    if (c == chunks - 1) {  // the shared group's chunk
+      const int last = a.E & 31;
+      const int at = __shfl_sync(0xffffffffu, cls < 4 ? first_group : INT_MAX, last);
+      const int n = __shfl_sync(0xffffffffu, tiles, last);
+      if (lane == 0) {
+        prefix[groups_all] = tiles_all;
+        *out = {groups_all, heavy, at, n};
+      }
     }
   }
 }
@@ -400,7 +417,7 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, EG, SPLIT>::T
   pdl_trigger();
   using C = Mx4Cfg<MODE, F4, CL, BN, STAGES, EG, SPLIT>;
   constexpr bool PAIR = CL == 2;
-  constexpr bool GROUPED = MODE != kLinearMx4;
+  constexpr bool GROUPED = MODE != kLinearMx4, FUSED = MODE == kExpertsMx4;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -409,9 +426,8 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, EG, SPLIT>::T
   uint64_t* bars = reinterpret_cast<uint64_t*>(epi + C::EPI_FLOATS);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + C::NBARS);
   volatile int* epi_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
-  int* n_sched = reinterpret_cast<int*>(tmem_holder + 2);
-  int* n_heavy = reinterpret_cast<int*>(tmem_holder + 3);
-  int32_t* prefix = reinterpret_cast<int32_t*>(tmem_holder + 4);
+  Mx4Schedule* sched = reinterpret_cast<Mx4Schedule*>(tmem_holder + 2);
+  int32_t* prefix = reinterpret_cast<int32_t*>(tmem_holder + 8);
   int32_t* offs = prefix + (args.E + 2);
   int32_t* order = offs + (args.E + 2);
 
@@ -442,13 +458,16 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, EG, SPLIT>::T
     fence_mbar_init();
   }
   if (warp == 0 && lane < (GROUPED ? 2 : 1)) {
-    tma_prefetch_desc(&args.tmA[lane]);
-    tma_prefetch_desc(&args.tmB[lane][0]);
-    if constexpr (PAIR) {
-      tma_prefetch_desc(&args.tmSA[lane]);
-      tma_prefetch_desc(&args.tmSB[lane]);
-      tma_prefetch_desc(&args.tmB[lane][1]);
-      tma_prefetch_desc(&args.tmB[lane][2]);
+    for (int p = 0; p < (FUSED ? 2 : 1); ++p) {
+      const Mx4Phase& f = args.ph[p];
+      tma_prefetch_desc(&f.tmA[lane]);
+      tma_prefetch_desc(&f.tmB[lane][0]);
+      if constexpr (PAIR) {
+        tma_prefetch_desc(&f.tmSA[lane]);
+        tma_prefetch_desc(&f.tmSB[lane]);
+        tma_prefetch_desc(&f.tmB[lane][1]);
+        tma_prefetch_desc(&f.tmB[lane][2]);
+      }
     }
   }
   if (warp == 1) {
@@ -459,8 +478,8 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, EG, SPLIT>::T
   }
   pdl_wait();  // global memory from here on
   if constexpr (GROUPED)  // scratch: the epilogue's buffers, not yet in use
-    build_schedule_block<128 * CL, C::THREADS>(args, BN, offs, order, prefix, n_sched, n_heavy,
-                                               reinterpret_cast<int32_t*>(epi));
+    build_schedule_block<C::THREADS>(args, BN, offs, order, prefix, sched,
+                                     reinterpret_cast<int32_t*>(epi));
   tc_fence_before();
   __syncthreads();
   if constexpr (PAIR) cluster_sync();
@@ -469,41 +488,62 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, EG, SPLIT>::T
   const uint32_t sf_cols = tmem_base + 2 * BN;
   const uint64_t limit = args.limit_ns;
 
-  int ngroups = 0, heavy_units = 0, total;
-  int lin_nb = 0, lin_mt = 0;
+  // Units of a phase before the i-th group of the order: its token tiles times
+  // the group's row blocks. The phases follow each other in the unit list.
+  int ngroups = 0, shared_at = 0, shared_tiles = 0, units0 = 0, heavy_units = 0, total;
+  auto row_blocks = [&](int p, int sh) {
+    return (args.ph[p].rows[sh] + 128 * CL - 1) / (128 * CL);
+  };
+  auto units_before = [&](int p, int i) {
+    return prefix[i] * row_blocks(p, 0) +
+           (i > shared_at ? shared_tiles * (row_blocks(p, 1) - row_blocks(p, 0)) : 0);
+  };
   if constexpr (GROUPED) {
-    ngroups = uniform(*n_sched);
-    heavy_units = uniform(*n_heavy);
-    total = uniform(prefix[ngroups]);
+    ngroups = uniform(sched->groups);
+    shared_at = uniform(sched->shared_at);
+    shared_tiles = uniform(sched->shared_tiles);
+    units0 = uniform(units_before(0, ngroups));
+    heavy_units = uniform(units_before(0, sched->heavy));
+    total = units0 + (FUSED ? uniform(units_before(1, ngroups)) : 0);
   } else {
-    lin_nb = (args.rows[0] + 128 * CL - 1) / (128 * CL);
-    lin_mt = (args.T + BN - 1) / BN;
-    total = lin_nb * lin_mt;
+    total = row_blocks(0, 0) * ((args.T + BN - 1) / BN);
   }
   auto compute_tile = [&](int u) {
     Mx4Tile t;
     int m, mt;
     if constexpr (GROUPED) {
-      const Tile tl =
-          decode_tile(remap_unit(u, total, heavy_units), prefix, order, offs, ngroups, BN);
-      t.g = tl.g;
-      t.nb = tl.nb * CL + crank;
-      mt = tl.mt;
-      m = offs[tl.g + 1] - offs[tl.g];
-      t.tb = tl.g == E ? 0 : (int)group_scale_tile(offs[tl.g], tl.g, BN);
-      t.p0 = tl.g == E ? 0 : offs[tl.g];  // the shared group's rows are in token order
+      t.phase = FUSED && u >= units0 ? 1 : 0;
+      // The two phases' lists hold light groups (decode-sized batches); a single
+      // one deals its heavy units evenly among the light ones.
+      u = FUSED ? u - (t.phase ? units0 : 0) : remap_unit(u, total, heavy_units);
+      int lo = 0, hi = ngroups;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (units_before(t.phase, mid) <= u) lo = mid;
+        else hi = mid;
+      }
+      const int g = order[lo], local = u - units_before(t.phase, lo);
+      m = offs[g + 1] - offs[g];
+      const int mtiles = (m + BN - 1) / BN;
+      t.g = g;
+      t.nb = local / mtiles;  // token tiles fastest: they share weights
+      mt = local - t.nb * mtiles;
+      t.nb = t.nb * CL + crank;
+      t.tb = g == E ? 0 : (int)group_scale_tile(offs[g], g, BN);
+      t.p0 = g == E ? 0 : offs[g];  // the shared group's rows are in token order
       t.s0 = 0;
-      t.s1 = (args.kt[tl.g == E] + C::KT_STAGE - 1) / C::KT_STAGE;
+      t.s1 = (args.ph[t.phase].kt[g == E] + C::KT_STAGE - 1) / C::KT_STAGE;
     } else {
       // Token tiles fastest, so that the CTAs at work share weight rows in L2.
+      const int lin_mt = (args.T + BN - 1) / BN;
+      t.phase = 0;
       t.g = 0;
       mt = u % lin_mt;
-      const int v = u / lin_mt;
-      t.nb = v * CL + crank;
+      t.nb = u / lin_mt * CL + crank;
       m = args.T;
       t.tb = 0;
       t.p0 = 0;
-      const int n = (args.kt[0] + C::KT_STAGE - 1) / C::KT_STAGE;
+      const int n = (args.ph[0].kt[0] + C::KT_STAGE - 1) / C::KT_STAGE;
       const int rank = SPLIT ? (int)cluster_ctarank() : 0;
       t.s0 = rank * n / splits;  // never empty: splits <= n
       t.s1 = (rank + 1) * n / splits;
@@ -526,6 +566,7 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, EG, SPLIT>::T
     }
     const int src = lt & 31;
     Mx4Tile t;
+    t.phase = FUSED ? uniform(__shfl_sync(0xffffffffu, mine.phase, src)) : 0;
     t.g = uniform(__shfl_sync(0xffffffffu, mine.g, src));
     t.nb = uniform(__shfl_sync(0xffffffffu, mine.nb, src));
     t.p0 = uniform(__shfl_sync(0xffffffffu, mine.p0, src));
@@ -558,7 +599,7 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, EG, SPLIT>::T
         tma_load_2d(dst, m, x, y, bar(b), pol);
     };
     auto row_block_of = [&](const Mx4Tile& t, int sh) {
-      return (sh || !GROUPED ? 0 : t.g * (args.rows[0] / 128)) + t.nb;
+      return (sh || !GROUPED ? 0 : t.g * (args.ph[t.phase].rows[0] / 128)) + t.nb;
     };
     Mx4Tile next = {};
     if (n_units > 0) next = tile_at(0);
@@ -573,8 +614,9 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, EG, SPLIT>::T
     bool peek = false;
     for (int lt = 0; lt < n_units && ok; ++lt) {
       const Mx4Tile t = next;
+      const Mx4Phase& f = args.ph[t.phase];
       const int sh = GROUPED && t.g == E ? 1 : 0;
-      const int kt = args.kt[sh];
+      const int kt = f.kt[sh];
       // The last row block of a pair may lie past the group's rows: it loads
       // what is there (another group's rows, or zeros) and stores nothing.
       const int rt = row_block_of(t, sh);
@@ -583,10 +625,25 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, EG, SPLIT>::T
       const int box = bsel == 2 ? C::BOX2 : (bsel == 1 ? C::BOX1 : C::B_ROWS);
       const uint32_t tx = C::NB * (C::A_TX + box * 128);
       const int b_row = t.p0 + crank * need;
-      const CUtensorMap *mA = &args.tmA[sh], *mB = &args.tmB[sh][bsel];
+      const CUtensorMap *mA = &f.tmA[sh], *mB = &f.tmB[sh][bsel];
       const int sa_row = rt * kt, sb_row = t.tb * kt * C::RA;
       const int s0 = t.s0, s1 = t.s1;
       if (lt + 1 < n_units) next = tile_at(lt + 1);
+      if constexpr (FUSED) {
+        // A down unit reads h rows that other CTAs wrote: all row blocks of this
+        // token tile's gate/up product have to be done. Those units come before
+        // any down unit in every CTA's list, and all CTAs are resident.
+        if (t.phase == 1) {
+          int there = 1;
+          if (el) {
+            const int need = args.ph[0].rows[sh] / 128;
+            there = wait_count_at_least(args.done + (sh ? args.done_shared : 0) + t.tb, need,
+                                        args.status, limit);
+            fence_proxy_async_global();  // the loads below are the async proxy's
+          }
+          if (!(ok = __all_sync(0xffffffffu, there))) break;
+        }
+      }
       for (int st = s0 + first; st < s1; ++st) {
         if (!(ok = warp_wait(empty_bar(s), ph, args.status, limit, peek))) break;
         const int sn = s + 1 == STAGES ? 0 : s + 1;
@@ -597,14 +654,14 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, EG, SPLIT>::T
           if constexpr (PAIR) {
             // Whole boxes of scale tiles: those past the row are not used.
             if (leader) mbar_arrive_expect_tx(full_bar(s), 2 * (tx + C::SA_BYTES + C::SB_BYTES));
-            load(dst + C::SA_OFF, &args.tmSA[sh], 0, sa_row + ks, s, pol_w);
-            load(dst + C::SB_OFF, &args.tmSB[sh], 0, sb_row + ks * C::RA, s, pol_t);
+            load(dst + C::SA_OFF, &f.tmSA[sh], 0, sa_row + ks, s, pol_w);
+            load(dst + C::SB_OFF, &f.tmSB[sh], 0, sb_row + ks * C::RA, s, pol_t);
           } else {
             const uint32_t n = (uint32_t)min(C::KT_STAGE, kt - ks) * 512u;
             mbar_arrive_expect_tx(full_bar(s), tx + n * (1 + C::RA));
-            bulk_load(dst + C::SA_OFF, args.sA[sh] + ((int64_t)sa_row + ks) * 512, n, full_bar(s),
+            bulk_load(dst + C::SA_OFF, f.sA[sh] + ((int64_t)sa_row + ks) * 512, n, full_bar(s),
                       pol_w);
-            bulk_load(dst + C::SB_OFF, args.sB[sh] + ((int64_t)sb_row + ks * C::RA) * 512,
+            bulk_load(dst + C::SB_OFF, f.sB[sh] + ((int64_t)sb_row + ks * C::RA) * 512,
                       n * C::RA, full_bar(s), pol_t);
           }
 #pragma unroll
@@ -648,7 +705,7 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, EG, SPLIT>::T
       if (n_units > 0) next = tile_at(0);
       for (int lt = 0; lt < n_units && ok; ++lt) {
         const Mx4Tile t = next;
-        const int kt = args.kt[GROUPED && t.g == E ? 1 : 0];
+        const int kt = args.ph[t.phase].kt[GROUPED && t.g == E ? 1 : 0];
         const int s0 = t.s0, s1 = t.s1;
         const uint32_t acc = lt & 1u;
         if (!(ok = warp_wait(tempty_bar(acc), ((lt >> 1) & 1u) ^ 1u, args.status, limit))) break;
@@ -724,7 +781,8 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, EG, SPLIT>::T
       if (!*epi_flag) break;  // every epilogue thread sees the same flag
       tc_fence_after();
       const uint32_t t_acc = tmem_base + lane_base + acc * BN;
-      const bool live = t.nb * 128 < args.rows[shared];  // a pair's block past the last one
+      const Mx4Phase& f = args.ph[t.phase];
+      const bool live = t.nb * 128 < f.rows[shared];  // a pair's block past the last one
       if constexpr (SPLIT) {
         // Partial sums to shared memory ([column][row], over the drained ring);
         // the cluster adds them below.
@@ -749,7 +807,7 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, EG, SPLIT>::T
           tmem_ld16(t_acc + c0, v);
 #pragma unroll
           for (int i = 0; i < 16; ++i) mine_buf[i * 36 + lane] = v[i];
-          if constexpr (MODE == kGatedMx4) {
+          if (MODE == kGatedMx4 || (FUSED && t.phase == 0)) {
             // Rows 0..63 are gate, 64..127 up, of features 64 nb ..: warps q and
             // q + 2 share 32 features, a block of h, which is quantized from
             // fp32; each takes 8 of the tokens.
@@ -774,9 +832,9 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, EG, SPLIT>::T
             const float inv = mx_inv_scale(byte);
             const int j = c0 + pt;
             if (j < t.n_valid) {
-              const int kt_out = args.rows[shared] / 256;  // I / 128
-              uint8_t* out = reinterpret_cast<uint8_t*>(shared ? args.out_shared : args.out);
-              uint8_t* osc = shared ? args.out_shared_s : args.out_s;
+              const int kt_out = f.rows[shared] / 256;  // I / 128
+              uint8_t* out = reinterpret_cast<uint8_t*>(shared ? f.out_shared : f.out);
+              uint8_t* osc = shared ? f.out_shared_s : f.out_s;
               uint2 codes = make_uint2(mx_encode4(hv[0] * inv, hv[1] * inv, hv[2] * inv, hv[3] * inv),
                                        mx_encode4(hv[4] * inv, hv[5] * inv, hv[6] * inv, hv[7] * inv));
               if (byte == 255u) codes = make_uint2(0, 0);  // a NaN block
@@ -796,22 +854,22 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, EG, SPLIT>::T
               const float4* src = reinterpret_cast<const float4*>(mine_buf + pt * 36 + part * 8);
               const float4 lo = src[0], hi = src[1];
               const float o[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-              if constexpr (MODE == kDownMx4) {
+              if constexpr (MODE == kDownMx4 || FUSED) {
                 // The warp's 32 features are a block of the position's slot row.
                 const uint32_t byte = slot_scale_byte(amax_of_four(o));
                 const float inv = mx_inv_scale(byte);
                 if (j < t.n_valid) {
                   const int64_t at = ((int64_t)(shared ? args.T * args.k : 0) + t.p0 + j) *
-                                         (args.rows[0] / 32) +
+                                         (f.rows[0] / 32) +
                                      t.nb * 4 + q;
-                  reinterpret_cast<uint4*>(args.out)[at * 4 + part] =
+                  reinterpret_cast<uint4*>(f.out)[at * 4 + part] =
                       make_uint4(slot_pair(o[0], o[1], inv), slot_pair(o[2], o[3], inv),
                                  slot_pair(o[4], o[5], inv), slot_pair(o[6], o[7], inv));
-                  if (part == 0) args.out_s[at] = (uint8_t)byte;
+                  if (part == 0) f.out_s[at] = (uint8_t)byte;
                 }
               } else if (j < t.n_valid) {
-                store_outputs(o, args.out, (int64_t)(t.p0 + j) * args.ld_out,
-                              t.nb * 128 + q * 32 + part * 8, args.rows[0], args.out_f32 != 0,
+                store_outputs(o, f.out, (int64_t)(t.p0 + j) * args.ld_out,
+                              t.nb * 128 + q * 32 + part * 8, f.rows[0], args.out_f32 != 0,
                               args.vec_out != 0);
               }
             }
@@ -827,6 +885,17 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, EG, SPLIT>::T
           mbar_arrive_relaxed_cluster(mapa_shared(tempty_bar(acc), 0));
         else
           mbar_arrive_relaxed(tempty_bar(acc));
+      }
+      if constexpr (FUSED) {
+        // This unit's h rows, stored by every epilogue thread, become visible at
+        // GPU scope and to the async proxy before the tile's count moves.
+        if (t.phase == 0) {
+          fence_proxy_async_global();
+          __threadfence();
+          named_barrier_sync(1, C::EPI_THREADS);
+          if (et == 0)
+            red_release_gpu_add(args.done + (shared ? args.done_shared : 0) + t.tb, 1);
+        }
       }
     }
   }
@@ -851,8 +920,8 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, EG, SPLIT>::T
         a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
       }
       const float o[4] = {a.x, a.y, a.z, a.w};
-      store_outputs(o, args.out, (int64_t)(t.p0 + i / 32) * args.ld_out,
-                    t.nb * 128 + (i % 32) * 4, args.rows[0], args.out_f32 != 0,
+      store_outputs(o, args.ph[0].out, (int64_t)(t.p0 + i / 32) * args.ld_out,
+                    t.nb * 128 + (i % 32) * 4, args.ph[0].rows[0], args.out_f32 != 0,
                     args.vec_out != 0);
     }
     cluster_sync();  // no CTA leaves while a peer reads its sums
@@ -885,9 +954,30 @@ cudaError_t launch_variant(const Mx4Args& a, int num_sms, size_t units, int spli
                         st, (unsigned)cluster, a);
 }
 
+// A launch whose blocks are all resident at once, chained to its predecessor.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_cooperative(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                               cudaStream_t st, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 // Token tiles: 32 or 64 rows on single CTAs (4 stages of 42 to 52 KB), 224 rows
 // on pairs (3 stages of 63 or 66 KB; two accumulators of 224 columns and the
-// scales fill tensor memory; two epilogue groups).
+// scales fill tensor memory; two epilogue groups). The layer's single-CTA tiles
+// run in launch_mx4_experts.
 template <int MODE, bool F4>
 cudaError_t launch_mx4(const Mx4Args& a, const Mx4Tiling& t, int num_sms, size_t units, int splits,
                        cudaStream_t st) {
@@ -898,10 +988,10 @@ cudaError_t launch_mx4(const Mx4Args& a, const Mx4Tiling& t, int num_sms, size_t
       return t.rows == 32
                  ? launch_variant<MODE, F4, 1, 32, 4, 1, true>(a, num_sms, units, splits, st)
                  : launch_variant<MODE, F4, 1, 64, 4, 1, true>(a, num_sms, units, splits, st);
-    if (t.rows == 64)
-      return launch_variant<MODE, F4, 1, 64, 4, 1, false>(a, num_sms, units, 1, st);
+    return t.rows == 32 ? launch_variant<MODE, F4, 1, 32, 4, 1, false>(a, num_sms, units, 1, st)
+                        : launch_variant<MODE, F4, 1, 64, 4, 1, false>(a, num_sms, units, 1, st);
   }
-  return launch_variant<MODE, F4, 1, 32, 4, 1, false>(a, num_sms, units, 1, st);
+  return cudaErrorInvalidValue;
 }
 
 struct TokenMaps {
@@ -913,7 +1003,7 @@ struct TokenMaps {
 
 // Operand maps and addresses of group kind i (0 routed, 1 shared).
 template <bool F4>
-bool set_tokens(Mx4Args& a, int i, const TokenMaps& t, const Mx4Tiling& tl) {
+bool set_tokens(Mx4Phase& a, int i, const TokenMaps& t, const Mx4Tiling& tl) {
   const uint64_t cols = (uint64_t)t.kt * (F4 ? 64 : 128);
   a.sB[i] = t.s;
   if (!tl.pairs) return make_tma_map(&a.tmB[i][0], t.q, MOE_DTYPE_E4M3, t.rows, cols, tl.rows);
@@ -925,7 +1015,7 @@ bool set_tokens(Mx4Args& a, int i, const TokenMaps& t, const Mx4Tiling& tl) {
 }
 
 template <bool F4>
-bool set_weights(Mx4Args& a, int i, const uint8_t* q, const uint8_t* s, uint64_t rows,
+bool set_weights(Mx4Phase& a, int i, const uint8_t* q, const uint8_t* s, uint64_t rows,
                  const Mx4Tiling& tl) {
   const int kt = a.kt[i];
   a.sA[i] = s;
@@ -946,55 +1036,66 @@ Mx4Tiling mx4_tiling(int64_t T, int tile) {
 
 namespace {
 
-template <int MODE>
-cudaError_t launch_grouped(const GemmProblem& p, const Mx4Weights& w, const Mx4Tokens& x,
-                           const int32_t* offsets, const Mx4Out& out, int* status,
-                           cudaStream_t st) {
-  constexpr bool GATED = MODE == kGatedMx4;
+// The operands of the gate/up (gated) or the down GEMM.
+bool set_phase(Mx4Phase& f, const GemmProblem& p, bool gated, const Mx4Weights& w,
+               const Mx4Tokens& x, const Mx4Out& out, const Mx4Tiling& tl) {
   const bool has_s = p.Is > 0;
-  Mx4Args a;
-  memset(&a, 0, sizeof(a));
-  a.kt[0] = (GATED ? p.H : p.I) / 128;
-  a.kt[1] = GATED || !has_s ? a.kt[0] : p.Is / 128;
-  a.rows[0] = GATED ? 2 * p.I : p.H;
-  a.rows[1] = GATED ? (has_s ? 2 * p.Is : 2 * p.I) : p.H;
+  f.kt[0] = (gated ? p.H : p.I) / 128;
+  f.kt[1] = gated || !has_s ? f.kt[0] : p.Is / 128;
+  f.rows[0] = gated ? 2 * p.I : p.H;
+  f.rows[1] = gated ? (has_s ? 2 * p.Is : 2 * p.I) : p.H;
+  f.out = out.routed;
+  f.out_s = out.routed_s;
+  f.out_shared = out.shared;
+  f.out_shared_s = out.shared_s;
   const int P = p.T * p.k;
-  const Mx4Tiling tl = mx4_tiling(p.T, p.tile);
-  const int bn = tl.rows;
-  const TokenMaps rt = {x.routed, x.routed_s, (uint64_t)P, a.kt[0],
-                        (uint64_t)group_scale_tile(P, p.E, bn) + 1};
-  const TokenMaps sh = {x.shared, x.shared_s, (uint64_t)p.T, a.kt[1],
-                        (uint64_t)((p.T + bn - 1) / bn)};
-  bool ok = set_weights<false>(a, 0, GATED ? w.gate_up : w.down, GATED ? w.s_gate_up : w.s_down,
-                               (uint64_t)p.E * a.rows[0], tl) &&
-            set_tokens<false>(a, 0, rt, tl);
-  if (ok && has_s)
-    ok = set_weights<false>(a, 1, GATED ? w.sh_gate_up : w.sh_down,
-                            GATED ? w.sh_s_gate_up : w.sh_s_down, (uint64_t)a.rows[1], tl) &&
-         set_tokens<false>(a, 1, sh, tl);
-  if (!ok) return cudaErrorInvalidValue;
-  if (!has_s) {
-    a.tmA[1] = a.tmA[0];
-    a.tmSA[1] = a.tmSA[0];
-    a.tmSB[1] = a.tmSB[0];
-    for (int i = 0; i < 3; ++i) a.tmB[1][i] = a.tmB[0][i];
+  const TokenMaps rt = {x.routed, x.routed_s, (uint64_t)P, f.kt[0],
+                        (uint64_t)group_scale_tile(P, p.E, tl.rows) + 1};
+  if (!set_weights<false>(f, 0, gated ? w.gate_up : w.down, gated ? w.s_gate_up : w.s_down,
+                          (uint64_t)p.E * f.rows[0], tl) ||
+      !set_tokens<false>(f, 0, rt, tl))
+    return false;
+  if (has_s) {
+    const TokenMaps sh = {x.shared, x.shared_s, (uint64_t)p.T, f.kt[1],
+                          (uint64_t)((p.T + tl.rows - 1) / tl.rows)};
+    return set_weights<false>(f, 1, gated ? w.sh_gate_up : w.sh_down,
+                              gated ? w.sh_s_gate_up : w.sh_s_down, (uint64_t)f.rows[1], tl) &&
+           set_tokens<false>(f, 1, sh, tl);
   }
+  f.tmA[1] = f.tmA[0];
+  f.tmSA[1] = f.tmSA[0];
+  f.tmSB[1] = f.tmSB[0];
+  for (int i = 0; i < 3; ++i) f.tmB[1][i] = f.tmB[0][i];
+  return true;
+}
+
+void set_problem(Mx4Args& a, const GemmProblem& p, const int32_t* offsets, int* status) {
   a.offsets = offsets;
-  a.out = out.routed;
-  a.out_s = out.routed_s;
-  a.out_shared = out.shared;
-  a.out_shared_s = out.shared_s;
   a.status = status;
   a.limit_ns = p.limit_ns;
   a.T = p.T;
   a.k = p.k;
   a.E = p.E;
-  a.KP = p.k + (has_s ? 1 : 0);
+  a.KP = p.k + (p.Is > 0 ? 1 : 0);
   a.flags = p.flags;
+}
+
+size_t phase_units(const GemmProblem& p, const Mx4Phase& f, const Mx4Tiling& tl) {
   const int ur = tl.pairs ? 256 : 128;  // weight rows of a unit
-  const size_t ub = unit_upper_bound(p.T, p.k, p.E, bn, (a.rows[0] + ur - 1) / ur,
-                                     has_s ? (a.rows[1] + ur - 1) / ur : 0);
-  return launch_mx4<MODE, false>(a, tl, p.num_sms, ub, 1, st);
+  return unit_upper_bound(p.T, p.k, p.E, tl.rows, (f.rows[0] + ur - 1) / ur,
+                          p.Is > 0 ? (f.rows[1] + ur - 1) / ur : 0);
+}
+
+template <int MODE>
+cudaError_t launch_grouped(const GemmProblem& p, const Mx4Weights& w, const Mx4Tokens& x,
+                           const int32_t* offsets, const Mx4Out& out, int* status,
+                           cudaStream_t st) {
+  Mx4Args a;
+  memset(&a, 0, sizeof(a));
+  const Mx4Tiling tl = mx4_tiling(p.T, p.tile);
+  if (!set_phase(a.ph[0], p, MODE == kGatedMx4, w, x, out, tl)) return cudaErrorInvalidValue;
+  set_problem(a, p, offsets, status);
+  return launch_mx4<MODE, false>(a, tl, p.num_sms, phase_units(p, a.ph[0], tl), 1, st);
 }
 
 }  // namespace
@@ -1010,6 +1111,37 @@ cudaError_t launch_mx4_down_gemm(const GemmProblem& p, const Mx4Weights& w, cons
                                  cudaStream_t st) {
   const Mx4Out out = {reinterpret_cast<uint8_t*>(y.q), y.s, nullptr, nullptr};
   return launch_grouped<kDownMx4>(p, w, h, offsets, out, status, st);
+}
+
+// Both GEMMs of a batch on single-CTA tiles in one cooperative launch: its CTAs
+// wait for one another's h rows, so all of them have to be resident.
+int64_t mx4_done_counters(int64_t T, int64_t k, int64_t E, int tile) {
+  const Mx4Tiling tl = mx4_tiling(T, tile);
+  return group_scale_tile(T * k, (int)E, tl.rows) + 1 + (T + tl.rows - 1) / tl.rows;
+}
+
+cudaError_t launch_mx4_experts(const GemmProblem& p, const Mx4Weights& w, const Mx4Tokens& x,
+                               const int32_t* offsets, const Mx4Out& h, const Mx4Slots& y,
+                               int* done, int* status, cudaStream_t st) {
+  const Mx4Tiling tl = mx4_tiling(p.T, p.tile);
+  if (tl.pairs) return cudaErrorInvalidValue;
+  Mx4Args a;
+  memset(&a, 0, sizeof(a));
+  const Mx4Tokens ht = {h.routed, h.routed_s, h.shared, h.shared_s};
+  const Mx4Out out = {reinterpret_cast<uint8_t*>(y.q), y.s, nullptr, nullptr};
+  if (!set_phase(a.ph[0], p, true, w, x, h, tl) || !set_phase(a.ph[1], p, false, w, ht, out, tl))
+    return cudaErrorInvalidValue;
+  set_problem(a, p, offsets, status);
+  a.done = done;
+  a.done_shared = (int)group_scale_tile((int64_t)p.T * p.k, p.E, tl.rows) + 1;
+  using C = Mx4Cfg<kExpertsMx4, false, 1, 32, 4, 1, false>;
+  auto fn = mx4_gemm_kernel<kExpertsMx4, false, 1, 32, 4, 1, false>;
+  cudaError_t e = ensure_smem_attr((const void*)fn, C::smem_bytes(kMaxExperts));
+  if (e != cudaSuccess) return e;
+  size_t n = phase_units(p, a.ph[0], tl) + phase_units(p, a.ph[1], tl);
+  if (n > (size_t)p.num_sms) n = (size_t)p.num_sms;
+  if (n == 0) return cudaSuccess;
+  return launch_cooperative(fn, dim3((unsigned)n), dim3(C::THREADS), C::smem_bytes(a.E), st, a);
 }
 
 // Tiling and clusters over K of a dense product.
@@ -1031,23 +1163,24 @@ Mx4LinearPlan mx4_linear_plan(int64_t T, int64_t N, int64_t K, int num_sms) {
 cudaError_t launch_mx4_linear(const Mx4Linear& l, cudaStream_t st) {
   Mx4Args a;
   memset(&a, 0, sizeof(a));
-  a.kt[0] = a.kt[1] = (int)mxfp4_k_tiles(l.K);
-  a.rows[0] = a.rows[1] = (int)l.N;
+  Mx4Phase& f = a.ph[0];
+  f.kt[0] = (int)mxfp4_k_tiles(l.K);
+  f.rows[0] = (int)l.N;
+  f.out = l.y;
   const Mx4Tiling& tl = l.plan.tiling;
-  const TokenMaps tm = {l.xq, l.xs, (uint64_t)l.T, a.kt[0],
+  const TokenMaps tm = {l.xq, l.xs, (uint64_t)l.T, f.kt[0],
                         (uint64_t)((l.T + tl.rows - 1) / tl.rows)};
-  const bool ok = l.e2m1 ? set_weights<true>(a, 0, l.wq, l.ws, l.N, tl) &&
-                               set_tokens<true>(a, 0, tm, tl)
-                         : set_weights<false>(a, 0, l.wq, l.ws, l.N, tl) &&
-                               set_tokens<false>(a, 0, tm, tl);
+  const bool ok = l.e2m1 ? set_weights<true>(f, 0, l.wq, l.ws, l.N, tl) &&
+                               set_tokens<true>(f, 0, tm, tl)
+                         : set_weights<false>(f, 0, l.wq, l.ws, l.N, tl) &&
+                               set_tokens<false>(f, 0, tm, tl);
   if (!ok) return cudaErrorInvalidValue;
   a.status = l.status;
   a.limit_ns = l.limit_ns;
   a.T = l.T;
-  a.out = l.y;
   a.ld_out = l.ld_y;
   a.out_f32 = l.y_f32;
-  a.vec_out = (reinterpret_cast<uintptr_t>(a.out) & 15u) == 0 &&
+  a.vec_out = (reinterpret_cast<uintptr_t>(l.y) & 15u) == 0 &&
               a.ld_out * (l.y_f32 ? 4 : 2) % 16 == 0;
   const int ur = tl.pairs ? 256 : 128;  // weight rows of a unit
   const size_t units = (size_t)((l.N + ur - 1) / ur) * ((l.T + tl.rows - 1) / tl.rows);

@@ -238,6 +238,8 @@ struct MxTokenArgs {
   const int32_t *slot_pos, *topk_ids, *offsets;
   int* status;
   int clear_status;  // set *status to MOE_OK (the first kernel of its call)
+  int* zero;         // routed: zeroed ints for a later kernel
+  int n_zero;
 };
 cudaError_t launch_quantize_tokens(const MxTokenArgs& args, bool routed, bool e2m1,
                                    cudaStream_t st);
@@ -266,6 +268,12 @@ cudaError_t launch_mx4_swiglu_gemm(const GemmProblem& p, const Mx4Weights& w, co
 cudaError_t launch_mx4_down_gemm(const GemmProblem& p, const Mx4Weights& w, const Mx4Tokens& h,
                                  const int32_t* offsets, const Mx4Slots& y, int* status,
                                  cudaStream_t st);
+// Both in one cooperative launch, for the tilings of single CTAs. done:
+// mx4_done_counters() zeros.
+int64_t mx4_done_counters(int64_t T, int64_t k, int64_t E, int tile);
+cudaError_t launch_mx4_experts(const GemmProblem& p, const Mx4Weights& w, const Mx4Tokens& x,
+                               const int32_t* offsets, const Mx4Out& h, const Mx4Slots& y,
+                               int* done, int* status, cudaStream_t st);
 // y[t] = sum over t's k slots of their gate weight times the slot, in rank
 // order, plus the shared expert's slot (positions T*k + t) when `shared`.
 cudaError_t launch_mx4_combine(const Mx4Slots& s, const int32_t* slot_pos, const float* topk_w,

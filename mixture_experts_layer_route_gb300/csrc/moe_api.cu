@@ -44,6 +44,7 @@ struct Layout {
   // (xq above holds the codes), their expert-ordered copies (xg holds the
   // codes), and the scale rows of h and h_shared (h, hs hold the codes).
   size_t xs, xgs, hsc, hss;
+  size_t done;  // MXFP4 layers on single-CTA tiles: the fused GEMMs' counters
   size_t ys;  // MXFP4 layers only: the slots' scales (Y holds their int16 codes)
   bool mx_dec;
   // MXFP4 layers: token codes in expert order (xg) with their scale tiles (xgs
@@ -158,6 +159,9 @@ Layout layout_of(const moe_problem& p) {
   L.shs = f8 && p.I_shared > 0 ? take(T * 4) : 0;
   L.Y = take(T * KP * (size_t)p.H * (m4 ? 2 : 4));
   L.ys = m4 ? take(T * KP * (size_t)(p.H / 32)) : 0;
+  L.done = m4 && !mx4_tiling(p.T, p.tile).pairs
+               ? take((size_t)mx4_done_counters(p.T, p.k, p.E, p.tile) * 4)
+               : 0;
   // Single-launch decode kernel: per-group counts of finished gate/up units.
   L.units = take((E + 2) * 4);
   // ... and its router partial sums (at most 8 slices of H), for decode-sized
@@ -863,6 +867,7 @@ moe_status moe_forward_mxfp4(const moe_problem* pb, const void* x, const void* W
   int32_t* offs = at<int32_t>(workspace, L.offsets);
   int32_t* gidx = at<int32_t>(workspace, L.gather);
   int32_t* spos = at<int32_t>(workspace, L.slotpos);
+  int* done = L.done ? at<int>(workspace, L.done) : nullptr;
   const Mx4Slots Y = {at<int16_t>(workspace, L.Y), at<uint8_t>(workspace, L.ys)};
   const Mx4Weights mw = {Wq_gate_up, s_gate_up, Wq_down, s_down,
                          Wsq_gate_up, ss_gate_up, Wsq_down, ss_down};
@@ -911,15 +916,24 @@ moe_status moe_forward_mxfp4(const moe_problem* pb, const void* x, const void* W
     a.topk_ids = ids;
     a.offsets = offs;
     a.status = status;
+    a.zero = done;
+    a.n_zero = done ? (int)mx4_done_counters(pb->T, pb->k, pb->E, pb->tile) : 0;
     e = launch_quantize_tokens(a, true, false, st);
   }
-  if (e == cudaSuccess) {
-    NvtxRange r("gate_up_gemm");
-    e = launch_mx4_swiglu_gemm(g, mw, xt, offs, ho, status, st);
-  }
-  if (e == cudaSuccess) {
-    NvtxRange r("down_gemm");
-    e = launch_mx4_down_gemm(g, mw, ht, offs, Y, status, st);
+  if (done) {
+    if (e == cudaSuccess) {
+      NvtxRange r("expert_gemms");
+      e = launch_mx4_experts(g, mw, xt, offs, ho, Y, done, status, st);
+    }
+  } else {
+    if (e == cudaSuccess) {
+      NvtxRange r("gate_up_gemm");
+      e = launch_mx4_swiglu_gemm(g, mw, xt, offs, ho, status, st);
+    }
+    if (e == cudaSuccess) {
+      NvtxRange r("down_gemm");
+      e = launch_mx4_down_gemm(g, mw, ht, offs, Y, status, st);
+    }
   }
   if (e == cudaSuccess) {
     NvtxRange r("combine");

@@ -258,6 +258,9 @@ __global__ void __launch_bounds__(256) quantize_tokens_kernel(MxTokenArgs a) {
   const int c8 = (int)(blockIdx.x - (unsigned)t * chunks) * 256 + (int)threadIdx.x;
   const int code_row = (E2M1 ? 64 : 128) * kt;
   if constexpr (ROUTED) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < a.n_zero;
+         i += (int64_t)gridDim.x * 256)
+      a.zero[i] = 0;
     if ((int)threadIdx.x < a.k) {
       const int64_t slot = (int64_t)t * a.k + threadIdx.x;
       const int p = a.slot_pos[slot], e = a.topk_ids[slot];
