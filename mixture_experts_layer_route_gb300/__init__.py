@@ -11,12 +11,15 @@ include/moe_api.h); this package only marshals torch tensors into it:
 """
 from __future__ import annotations
 
+import math
+
 import torch
 
 from ._binding import (  # noqa: F401
     EXPORTED, MOE_DTYPE_BF16, MOE_DTYPE_E4M3, MOE_DTYPE_F32, MOE_DTYPE_MXFP4, MOE_DTYPE_MXFP8,
     MOE_FLAG_TEST_SKIP_SIGNAL, MOE_OK, MOE_TILE_AUTO, MOE_TILE_DECODE, MOE_TILE_MEDIUM,
-    MOE_TILE_PREFILL, STATUS_NAMES, MoEError, MoEProblem, _check_mxfp4, _linear_mxfp4, dequantize_mxfp4,
+    MOE_TILE_PREFILL, STATUS_NAMES, MoEError, MoEProblem, _check_mxfp4, _linear_mxfp4, _quantize_mxfp4,
+    dequantize_mxfp4,
     down_combine, down_combine_noalloc, forward, forward_fp8, forward_mx, forward_mxfp4,
     forward_single_launch, get_device_status, grouped_swiglu_gemm, linear_mxfp4,
     linear_mxfp4_workspace_size, load_library, make_problem, mx_scale_cols, mxfp4_code_cols,
@@ -176,10 +179,11 @@ def quantize_mxfp4_rows(W: torch.Tensor, stream=None):
     power-of-two scale per block of 32 elements). A matrix may have any row
     stride; W of more dimensions is contiguous."""
     *lead, cols = W.shape
-    rows = W.numel() // cols
-    q = torch.empty((*lead, mxfp4_code_cols(cols)), dtype=torch.uint8, device=W.device)
-    s = torch.empty(mxfp4_scale_bytes(rows, cols), dtype=torch.uint8, device=W.device)
-    quantize_mxfp4(W if W.dim() == 2 else W.view(rows, cols), q, s, stream)
+    rows = math.prod(lead)
+    device = W.device
+    q = torch.empty((*lead, mxfp4_code_cols(cols)), dtype=torch.uint8, device=device)
+    s = torch.empty(mxfp4_scale_bytes(rows, cols), dtype=torch.uint8, device=device)
+    _quantize_mxfp4(W if len(lead) == 1 else W.view(rows, cols), q, s, stream)
     return q, s
 
 
@@ -212,6 +216,7 @@ class LinearMXFP4:
             raise ValueError(f"act: 'mxfp8' or 'mxfp4' expected, got {act!r}")
         _check_mxfp4(q, s, N, K, "W")
         self.q, self.s, self.N, self.K = q, s, N, K
+        self._q_ptr, self._s_ptr = q.data_ptr(), s.data_ptr()
         self.act = MOE_DTYPE_MXFP8 if act == "mxfp8" else MOE_DTYPE_MXFP4
         self._ws = {}
 
@@ -225,14 +230,17 @@ class LinearMXFP4:
 
     def forward(self, x, out=None, stream=None, out_f32=False):
         """y [T, N], bf16 or (out_f32) fp32, for x [T, K] of any row stride."""
-        if x.dim() != 2 or x.shape[1] != self.K:
-            raise ValueError(f"x: [T, {self.K}] expected, got {tuple(x.shape)}")
-        T = x.shape[0]
+        shape = x.shape
+        if len(shape) != 2 or shape[1] != self.K:
+            raise ValueError(f"x: [T, {self.K}] expected, got {tuple(shape)}")
+        T = shape[0]
         odt = torch.float32 if out_f32 else torch.bfloat16
         y = out if out is not None else torch.empty((T, self.N), dtype=odt, device=x.device)
-        ws = self.workspace(T)
-        _linear_mxfp4(x, self.act, self.q.data_ptr(), self.s.data_ptr(), self.N, y,
-                      ws.data_ptr(), ws.numel(), stream)
+        ws = self._ws.get(T)
+        if ws is None:
+            ws = self.workspace(T)
+        _linear_mxfp4(x, self.act, self._q_ptr, self._s_ptr, self.N, y, ws.data_ptr(), ws.numel(),
+                      stream)
         return y
 
     __call__ = forward

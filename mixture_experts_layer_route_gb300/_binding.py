@@ -136,7 +136,7 @@ def _ptr(t) -> int | None:
 
 def _stream(stream) -> int | None:
     if stream is None:  # the raw handle: a Stream object costs ~3 us a call
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -284,23 +284,26 @@ _FLOAT_DTYPES = {torch.bfloat16: MOE_DTYPE_BF16, torch.float32: MOE_DTYPE_F32}
 
 
 def _float_rows(t, name: str):
-    """(MOE_DTYPE, row stride) of a bf16 or fp32 matrix with contiguous rows."""
+    """(MOE_DTYPE, rows, cols, row stride) of a bf16 or fp32 matrix with
+    contiguous rows."""
     dt = _FLOAT_DTYPES.get(t.dtype)
     if dt is None:
         raise ValueError(f"{name}: bf16 or fp32 expected, got {t.dtype}")
-    if t.dim() != 2:
-        raise ValueError(f"{name}: a matrix expected, got {tuple(t.shape)}")
-    rows, cols = t.shape
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name}: a matrix expected, got {tuple(shape)}")
+    rows, cols = shape
     ld, inner = t.stride()
-    if cols > 1 and inner != 1:
+    if inner != 1 and cols > 1:
         raise ValueError(f"{name}: contiguous rows expected, got strides {(ld, inner)}")
-    return dt, ld if rows > 1 else cols
+    return dt, rows, cols, ld if rows > 1 else cols
 
 
 def _check_mxfp4(q, scales, rows: int, cols: int, name: str):
     """Codes and scales are contiguous bytes of the sizes [rows, cols] has."""
-    for t, n in ((q, rows * mxfp4_code_cols(cols)), (scales, mxfp4_scale_bytes(rows, cols))):
-        if t.dtype != torch.uint8 or not t.is_contiguous() or t.numel() != n:
+    kt = -(-cols // 128)
+    for t, n in ((q, rows * kt * 64), (scales, -(-rows // 128) * kt * 512)):
+        if t.numel() != n or t.dtype != torch.uint8 or not t.is_contiguous():
             raise ValueError(f"{name}: {n} contiguous bytes expected for [{rows}, {cols}], got "
                              f"{t.numel()} of {t.dtype}")
 
@@ -309,11 +312,16 @@ def quantize_mxfp4(src, q, scales, stream=None):
     """MXFP4 codes q [rows, mxfp4_code_cols(cols)] and tiled scales
     (mxfp4_scale_bytes(rows, cols) bytes) of src [rows, cols] (bf16 or fp32,
     contiguous rows, any row stride), as moe_quantize_mxfp4 defines them."""
-    dt, ld = _float_rows(src, "src")
-    rows, cols = src.shape
-    _check_mxfp4(q, scales, rows, cols, "q, scales")
-    _check("moe_quantize_mxfp4", load_library().moe_quantize_mxfp4(
-        src.data_ptr(), dt, rows, cols, ld, q.data_ptr(), scales.data_ptr(), _stream(stream)))
+    _check_mxfp4(q, scales, *src.shape, "q, scales")
+    _quantize_mxfp4(src, q, scales, stream)
+
+
+def _quantize_mxfp4(src, q, scales, stream):
+    dt, rows, cols, ld = _float_rows(src, "src")
+    code = load_library().moe_quantize_mxfp4(src.data_ptr(), dt, rows, cols, ld, q.data_ptr(),
+                                             scales.data_ptr(), _stream(stream))
+    if code:
+        raise MoEError("moe_quantize_mxfp4", code)
 
 
 def quantize_mxfp4_gate_up(W_gate, W_up, q, scales, stream=None):
@@ -323,7 +331,7 @@ def quantize_mxfp4_gate_up(W_gate, W_up, q, scales, stream=None):
     if W_up.shape != W_gate.shape or W_up.dtype != W_gate.dtype or not (
             W_gate.is_contiguous() and W_up.is_contiguous()):
         raise ValueError("W_gate, W_up: two contiguous tensors of one shape and dtype expected")
-    dt, _ = _float_rows(W_gate.view(E * I, H), "W_gate")
+    dt = _float_rows(W_gate.view(E * I, H), "W_gate")[0]
     _check_mxfp4(q, scales, 2 * E * I, H, "q, scales")
     _check("moe_quantize_mxfp4_gate_up", load_library().moe_quantize_mxfp4_gate_up(
         _ptr(W_gate), _ptr(W_up), dt, E, I, H, _ptr(q), _ptr(scales), _stream(stream)))
@@ -332,11 +340,12 @@ def quantize_mxfp4_gate_up(W_gate, W_up, q, scales, stream=None):
 def dequantize_mxfp4(q, scales, out, stream=None):
     """out [rows, cols] (bf16 or fp32, any row stride): the values of an MXFP4
     matrix (moe_dequantize_mxfp4)."""
-    dt, ld = _float_rows(out, "out")
-    rows, cols = out.shape
+    dt, rows, cols, ld = _float_rows(out, "out")
     _check_mxfp4(q, scales, rows, cols, "q, scales")
-    _check("moe_dequantize_mxfp4", load_library().moe_dequantize_mxfp4(
-        q.data_ptr(), scales.data_ptr(), rows, cols, out.data_ptr(), dt, ld, _stream(stream)))
+    code = load_library().moe_dequantize_mxfp4(q.data_ptr(), scales.data_ptr(), rows, cols,
+                                               out.data_ptr(), dt, ld, _stream(stream))
+    if code:
+        raise MoEError("moe_dequantize_mxfp4", code)
 
 
 def linear_mxfp4_workspace_size(T: int, N: int, K: int, act: int) -> int:
@@ -356,16 +365,16 @@ def linear_mxfp4(x, act: int, Wq, s_W, N: int, y, workspace, stream=None):
 
 def _linear_mxfp4(x, act, Wq, s_W, N, y, workspace, workspace_bytes, stream):
     """linear_mxfp4 with the addresses of checked weights and workspace."""
-    xdt, ld_x = _float_rows(x, "x")
+    xdt, T, K, ld_x = _float_rows(x, "x")
     if xdt != MOE_DTYPE_BF16:
         raise ValueError("x: bf16 expected")
-    dt, ld_y = _float_rows(y, "y")
-    T, K = x.shape
-    if y.shape != (T, N):
+    dt, rows, cols, ld_y = _float_rows(y, "y")
+    if rows != T or cols != N:
         raise ValueError(f"y: shape {(T, N)} expected, got {tuple(y.shape)}")
-    _check("moe_linear_mxfp4", load_library().moe_linear_mxfp4(
-        x.data_ptr(), T, K, ld_x, act, Wq, s_W, N, y.data_ptr(), dt, ld_y, workspace,
-        workspace_bytes, _stream(stream)))
+    code = load_library().moe_linear_mxfp4(x.data_ptr(), T, K, ld_x, act, Wq, s_W, N, y.data_ptr(),
+                                           dt, ld_y, workspace, workspace_bytes, _stream(stream))
+    if code:
+        raise MoEError("moe_linear_mxfp4", code)
 
 
 def forward_mxfp4(problem, x, W_router, router_bias, Wq_gate_up, s_gate_up, Wq_down, s_down,
