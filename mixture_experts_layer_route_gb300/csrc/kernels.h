@@ -211,10 +211,9 @@ cudaError_t launch_mx_dec_down_gemm(const GemmProblem& p, const MxWeights& w,
 // counts both).
 cudaError_t launch_quantize_mxfp4(int dtype, const void* src, const void* src2, int64_t rows,
                                   int64_t cols, int64_t ld, int64_t I, uint8_t* q, uint8_t* scales,
-                                  int num_sms, cudaStream_t st);
+                                  cudaStream_t st);
 cudaError_t launch_dequantize_mxfp4(const uint8_t* q, const uint8_t* scales, int64_t rows,
-                                    int64_t cols, int dtype, void* out, int64_t ld, int num_sms,
-                                    cudaStream_t st);
+                                    int64_t cols, int dtype, void* out, int64_t ld, cudaStream_t st);
 // Token tiles of an MXFP4 product (gemm_mxfp4.cu; mx4_tiling: of the layer's
 // grouped ones): at most `rows` rows, cut in
 // multiples of `unit`, with `row_atoms` 128-row scale tiles each.

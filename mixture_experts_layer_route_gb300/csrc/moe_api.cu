@@ -952,7 +952,8 @@ namespace {
 // Extents of an MXFP4 matrix: 32-bit tensor-map coordinates and k tiles.
 bool mxfp4_extents_ok(int64_t rows, int64_t cols) {
   const int64_t lim = (int64_t)1 << 30;
-  return rows < lim && cols < lim && (rows + 127) / 128 * mxfp4_k_tiles(cols) < lim;
+  return rows < lim && cols < ((int64_t)1 << 27) &&
+         (rows + 127) / 128 * mxfp4_k_tiles(cols) < lim;
 }
 }  // namespace
 
@@ -968,7 +969,7 @@ moe_status moe_quantize_mxfp4(const void* src, int32_t src_dtype, int64_t rows, 
   if (reinterpret_cast<uintptr_t>(src) % es != 0 || !aligned16(q) || !aligned16(scales))
     return MOE_ERR_INVALID_ARG;
   return cuda_status(launch_quantize_mxfp4(src_dtype, src, nullptr, rows, cols, ld, 0, q, scales,
-                                           sm_count(), (cudaStream_t)stream));
+                                           (cudaStream_t)stream));
 }
 
 moe_status moe_quantize_mxfp4_gate_up(const void* W_gate, const void* W_up, int32_t src_dtype,
@@ -985,7 +986,7 @@ moe_status moe_quantize_mxfp4_gate_up(const void* W_gate, const void* W_up, int3
   for (const void* p : ptrs)
     if (!p || !aligned16(p)) return MOE_ERR_INVALID_ARG;
   return cuda_status(launch_quantize_mxfp4(src_dtype, W_gate, W_up, 2 * E * I, H, H, I, q, scales,
-                                           sm_count(), (cudaStream_t)stream));
+                                           (cudaStream_t)stream));
 }
 
 moe_status moe_dequantize_mxfp4(const uint8_t* q, const uint8_t* scales, int64_t rows, int64_t cols,
@@ -999,7 +1000,7 @@ moe_status moe_dequantize_mxfp4(const uint8_t* q, const uint8_t* scales, int64_t
   const uintptr_t es = out_dtype == MOE_DTYPE_BF16 ? 2 : 4;
   if (reinterpret_cast<uintptr_t>(out) % es != 0 || !aligned16(q) || !aligned16(scales))
     return MOE_ERR_INVALID_ARG;
-  return cuda_status(launch_dequantize_mxfp4(q, scales, rows, cols, out_dtype, out, ld, sm_count(),
+  return cuda_status(launch_dequantize_mxfp4(q, scales, rows, cols, out_dtype, out, ld,
                                              (cudaStream_t)stream));
 }
 

@@ -15,7 +15,6 @@
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
-#include <cuda_fp4.h>
 #include <cuda_fp8.h>
 
 #include <cstdint>
@@ -103,16 +102,38 @@ __device__ __forceinline__ float2 slot_codes(uint32_t pair) {
                      __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7632)) - off);
 }
 
-// Two values -> two E2M1 codes in a byte (nearest even, saturating at 6).
-__device__ __forceinline__ uint32_t e2m1_pair(float lo, float hi) {
-  return (uint32_t)__nv_cvt_float2_to_fp4x2(make_float2(lo, hi), __NV_E2M1, cudaRoundNearest);
+// Eight values -> eight E2M1 codes (nearest even, saturating at 6), the first in
+// the lowest four bits.
+__device__ __forceinline__ uint32_t e2m1_encode8(const float (&v)[8]) {
+  uint32_t w;
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+      "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+      : "=r"(w)
+      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+  return w;
 }
 
-// A byte of two E2M1 codes -> their values.
-__device__ __forceinline__ float2 e2m1_values(uint32_t byte) {
-  const __half2_raw hr =
-      __nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)(byte & 0xFFu), __NV_E2M1);
-  return __half22float2(*reinterpret_cast<const __half2*>(&hr));
+// Eight E2M1 codes -> their values (exact in fp16).
+__device__ __forceinline__ void e2m1_decode8(uint32_t w, float (&v)[8]) {
+  uint32_t h[4];
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
+  }
 }
 
 // The scale 2^(byte - 127) of an E8M0 byte; 255 is NaN.
