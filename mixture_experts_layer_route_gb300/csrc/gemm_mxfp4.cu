@@ -86,9 +86,9 @@ struct Mx4Args {
   int out_f32, vec_out;
 };
 
-template <int MODE, bool F4, int CL, int BN, int STAGES, int EG, bool SPLIT>
+template <int MODE, bool F4, int CL, int BN, int STAGES, int NB_, int EG, bool SPLIT>
 struct Mx4Cfg {
-  static constexpr int NB = 2;                         // boxes per stage
+  static constexpr int NB = NB_;                       // boxes per stage
   static constexpr int KT_BOX = F4 ? 2 : 1;            // k tiles per box
   static constexpr int KT_STAGE = NB * KT_BOX;
   static constexpr int RA = (BN + 127) / 128;          // 128-row scale tiles per token tile
@@ -102,7 +102,7 @@ struct Mx4Cfg {
   static constexpr int SA_OFF = B_OFF + NB * B_BOX;
   static constexpr int SA_BYTES = KT_STAGE * 512, SB_BYTES = KT_STAGE * RA * 512;
   static constexpr int SB_OFF = SA_OFF + SA_BYTES;
-  static constexpr int STAGE_BYTES = SB_OFF + SB_BYTES;
+  static constexpr int STAGE_BYTES = (SB_OFF + SB_BYTES + 1023) / 1024 * 1024;
   // Tensor-memory columns of one box's scales (two ranges, by box parity).
   static constexpr int SF_COLS = KT_BOX * 4 * (1 + RA);
   static constexpr int USED_COLS = 2 * BN + 2 * SF_COLS;
@@ -411,11 +411,11 @@ __device__ __forceinline__ void build_schedule_block(const Mx4Args& a, int tile_
   }
 }
 
-template <int MODE, bool F4, int CL, int BN, int STAGES, int EG, bool SPLIT>
-__global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, EG, SPLIT>::THREADS, 1)
+template <int MODE, bool F4, int CL, int BN, int STAGES, int NB_, int EG, bool SPLIT>
+__global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, NB_, EG, SPLIT>::THREADS, 1)
     mx4_gemm_kernel(const __grid_constant__ Mx4Args args) {
   pdl_trigger();
-  using C = Mx4Cfg<MODE, F4, CL, BN, STAGES, EG, SPLIT>;
+  using C = Mx4Cfg<MODE, F4, CL, BN, STAGES, NB_, EG, SPLIT>;
   constexpr bool PAIR = CL == 2;
   constexpr bool GROUPED = MODE != kLinearMx4, FUSED = MODE == kExpertsMx4;
   extern __shared__ uint8_t smem_raw[];
@@ -699,7 +699,7 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, EG, SPLIT>::T
       // Operand descriptors differ in their start addresses only.
       const uint64_t dbase = umma_desc_sw128(stages_base), sbase = scale_tile_desc(stages_base);
       int s = 0;
-      uint32_t ph = 0;
+      uint32_t ph = 0, par = 0;
       bool ok = true, peek = false;
       Mx4Tile next = {};
       if (n_units > 0) next = tile_at(0);
@@ -725,7 +725,8 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, EG, SPLIT>::T
 #pragma unroll
             for (int b = 0; b < C::NB; ++b) {
               if (b * C::KT_BOX >= nk) break;
-              const uint32_t sa = sf_cols + b * C::SF_COLS, sb = sa + C::KT_BOX * 4;
+              const uint32_t sa = sf_cols + ((par + b) & 1u) * C::SF_COLS;
+              const uint32_t sb = sa + C::KT_BOX * 4;
               const uint64_t ad = dbase + (at + (b * C::A_BOX >> 4));
               const uint64_t bd = dbase + (at + ((C::B_OFF + b * C::B_BOX) >> 4));
               const uint64_t sad = sbase + (at + ((C::SA_OFF + b * C::KT_BOX * 512) >> 4));
@@ -750,6 +751,7 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, EG, SPLIT>::T
           }
           __syncwarp();
           accumulate = 1;
+          par ^= C::NB & 1u;
           if (++s == STAGES) s = 0, ph ^= 1u;
         }
         if (!ok) break;
@@ -938,12 +940,12 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, EG, SPLIT>::T
 constexpr int kMaxExperts = 1024;  // the C ABI's limit on E
 constexpr int kPairTile = 224;
 
-template <int MODE, bool F4, int CL, int BN, int STAGES, int EG, bool SPLIT>
+template <int MODE, bool F4, int CL, int BN, int STAGES, int NB_, int EG, bool SPLIT>
 cudaError_t launch_variant(const Mx4Args& a, int num_sms, size_t units, int splits,
                            cudaStream_t st) {
-  using C = Mx4Cfg<MODE, F4, CL, BN, STAGES, EG, SPLIT>;
+  using C = Mx4Cfg<MODE, F4, CL, BN, STAGES, NB_, EG, SPLIT>;
   static_assert(CL == 1 || CL == 2, "single CTAs or pairs");
-  auto fn = mx4_gemm_kernel<MODE, F4, CL, BN, STAGES, EG, SPLIT>;
+  auto fn = mx4_gemm_kernel<MODE, F4, CL, BN, STAGES, NB_, EG, SPLIT>;
   cudaError_t e = ensure_smem_attr((const void*)fn, C::smem_bytes(kMaxExperts));
   if (e != cudaSuccess) return e;
   if (units == 0) return cudaSuccess;
@@ -982,14 +984,14 @@ template <int MODE, bool F4>
 cudaError_t launch_mx4(const Mx4Args& a, const Mx4Tiling& t, int num_sms, size_t units, int splits,
                        cudaStream_t st) {
   if (t.pairs)
-    return launch_variant<MODE, F4, 2, kPairTile, 3, 2, false>(a, num_sms, units, 1, st);
+    return launch_variant<MODE, F4, 2, kPairTile, 6, 1, 2, false>(a, num_sms, units, 1, st);
   if constexpr (MODE == kLinearMx4) {
     if (splits > 1)
       return t.rows == 32
-                 ? launch_variant<MODE, F4, 1, 32, 4, 1, true>(a, num_sms, units, splits, st)
-                 : launch_variant<MODE, F4, 1, 64, 4, 1, true>(a, num_sms, units, splits, st);
-    return t.rows == 32 ? launch_variant<MODE, F4, 1, 32, 4, 1, false>(a, num_sms, units, 1, st)
-                        : launch_variant<MODE, F4, 1, 64, 4, 1, false>(a, num_sms, units, 1, st);
+                 ? launch_variant<MODE, F4, 1, 32, 4, 2, 1, true>(a, num_sms, units, splits, st)
+                 : launch_variant<MODE, F4, 1, 64, 4, 2, 1, true>(a, num_sms, units, splits, st);
+    return t.rows == 32 ? launch_variant<MODE, F4, 1, 32, 4, 2, 1, false>(a, num_sms, units, 1, st)
+                        : launch_variant<MODE, F4, 1, 64, 4, 2, 1, false>(a, num_sms, units, 1, st);
   }
   return cudaErrorInvalidValue;
 }
@@ -1007,7 +1009,7 @@ bool set_tokens(Mx4Phase& a, int i, const TokenMaps& t, const Mx4Tiling& tl) {
   const uint64_t cols = (uint64_t)t.kt * (F4 ? 64 : 128);
   a.sB[i] = t.s;
   if (!tl.pairs) return make_tma_map(&a.tmB[i][0], t.q, MOE_DTYPE_E4M3, t.rows, cols, tl.rows);
-  using C = Mx4Cfg<kDownMx4, F4, 2, kPairTile, 3, 1, false>;
+  using C = Mx4Cfg<kDownMx4, F4, 2, kPairTile, 6, 1, 2, false>;
   return make_tma_map(&a.tmB[i][0], t.q, MOE_DTYPE_E4M3, t.rows, cols, C::B_ROWS) &&
          make_tma_map(&a.tmB[i][1], t.q, MOE_DTYPE_E4M3, t.rows, cols, C::BOX1) &&
          make_tma_map(&a.tmB[i][2], t.q, MOE_DTYPE_E4M3, t.rows, cols, C::BOX2) &&
@@ -1022,7 +1024,7 @@ bool set_weights(Mx4Phase& a, int i, const uint8_t* q, const uint8_t* s, uint64_
   const bool ok = F4 ? make_tma_map(&a.tmA[i], q, MOE_DTYPE_E4M3, rows, (uint64_t)kt * 64, 128)
                      : make_spread_code_map(&a.tmA[i], q, rows, (uint64_t)kt * 128, 128);
   return ok &&
-         (!tl.pairs || make_scale_tile_map(&a.tmSA[i], s, (rows + 127) / 128 * kt, F4 ? 4 : 2));
+         (!tl.pairs || make_scale_tile_map(&a.tmSA[i], s, (rows + 127) / 128 * kt, F4 ? 2 : 1));
 }
 
 }  // namespace
@@ -1134,8 +1136,8 @@ cudaError_t launch_mx4_experts(const GemmProblem& p, const Mx4Weights& w, const 
   set_problem(a, p, offsets, status);
   a.done = done;
   a.done_shared = (int)group_scale_tile((int64_t)p.T * p.k, p.E, tl.rows) + 1;
-  using C = Mx4Cfg<kExpertsMx4, false, 1, 32, 4, 1, false>;
-  auto fn = mx4_gemm_kernel<kExpertsMx4, false, 1, 32, 4, 1, false>;
+  using C = Mx4Cfg<kExpertsMx4, false, 1, 32, 4, 2, 1, false>;
+  auto fn = mx4_gemm_kernel<kExpertsMx4, false, 1, 32, 4, 2, 1, false>;
   cudaError_t e = ensure_smem_attr((const void*)fn, C::smem_bytes(kMaxExperts));
   if (e != cudaSuccess) return e;
   size_t n = phase_units(p, a.ph[0], tl) + phase_units(p, a.ph[1], tl);
