@@ -55,12 +55,18 @@ namespace {
 // kExpertsMx4: the gate/up and the down GEMM as two phases of one launch.
 enum Mx4Mode : int { kGatedMx4 = 0, kDownMx4 = 1, kLinearMx4 = 2, kExpertsMx4 = 3 };
 
+// Heights of a pair's token boxes (rows per CTA): a tile loads the smallest that
+// covers its half of the columns (even cuts of 129 to 224 rows take 80 to 112).
+__host__ __device__ constexpr int pair_box(int i) {
+  return i == 0 ? 112 : (i == 1 ? 96 : (i == 2 ? 80 : (i == 3 ? 64 : 32)));
+}
+
 // The operands and outputs of one GEMM; [0] routed, [1] shared group.
 struct Mx4Phase {
-  // Pairs: token boxes of B_ROWS, BOX1 and BOX2 rows and maps of the scale
-  // tiles; single CTAs: one token box (tmB[.][0]), and the scale tiles as plain
-  // addresses (contiguous copies).
-  CUtensorMap tmA[2], tmB[2][3], tmSA[2], tmSB[2];
+  // Pairs: token boxes of 112, 96, 80, 64 and 32 rows (pair_box) and maps of the
+  // scale tiles; single CTAs: one token box (tmB[.][0]), and the scale tiles as
+  // plain addresses (contiguous copies).
+  CUtensorMap tmA[2], tmB[2][5], tmSA[2], tmSB[2];
   const uint8_t *sA[2], *sB[2];
   int rows[2];                // weight rows per group (GATED: 2 I)
   int kt[2];                  // k tiles (of 128) of the contraction
@@ -95,7 +101,6 @@ struct Mx4Cfg {
   static constexpr int A_BOX = 128 * 128;
   static constexpr int A_TX = F4 ? A_BOX : A_BOX / 2;  // bytes the load counts
   static constexpr int B_ROWS = BN / CL;
-  static constexpr int BOX1 = CL == 2 ? 64 : B_ROWS, BOX2 = CL == 2 ? 32 : B_ROWS;
   static constexpr int N_UNIT = 16 * CL;
   static constexpr int B_BOX = B_ROWS * 128;
   static constexpr int B_OFF = NB * A_BOX;
@@ -110,7 +115,9 @@ struct Mx4Cfg {
   static constexpr int EPI_GROUPS = EG;
   static constexpr int EPI_THREADS = 128 * EG;
   static constexpr int THREADS = 64 + EPI_THREADS;
-  static constexpr int EPI_BUF = 16 * 36;  // floats per epilogue warp: 16 tokens x 32 rows, padded
+  // Floats per epilogue warp: 16 tokens x 32 rows, padded so that eight lanes
+  // reading 16 bytes each, of one warp's buffer or of two, hit distinct banks.
+  static constexpr int EPI_BUF = 16 * 36 + 4;
   static constexpr int EPI_FLOATS = EG * 4 * EPI_BUF;
   // full, empty [STAGES]; tfull, tempty [2]; drain
   static constexpr int NBARS = 2 * STAGES + 5;
@@ -465,8 +472,7 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, NB_, EG, SPLI
       if constexpr (PAIR) {
         tma_prefetch_desc(&f.tmSA[lane]);
         tma_prefetch_desc(&f.tmSB[lane]);
-        tma_prefetch_desc(&f.tmB[lane][1]);
-        tma_prefetch_desc(&f.tmB[lane][2]);
+        for (int i = 1; i < 5; ++i) tma_prefetch_desc(&f.tmB[lane][i]);
       }
     }
   }
@@ -621,8 +627,9 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, NB_, EG, SPLI
       // what is there (another group's rows, or zeros) and stores nothing.
       const int rt = row_block_of(t, sh);
       const int need = mma_cols(t) / CL;
-      const int bsel = !PAIR || need > C::BOX1 ? 0 : (need > C::BOX2 ? 1 : 2);
-      const int box = bsel == 2 ? C::BOX2 : (bsel == 1 ? C::BOX1 : C::B_ROWS);
+      int bsel = 0;
+      if constexpr (PAIR) bsel = need > 96 ? 0 : (need > 80 ? 1 : (need > 64 ? 2 : (need > 32 ? 3 : 4)));
+      const int box = PAIR ? pair_box(bsel) : C::B_ROWS;
       const uint32_t tx = C::NB * (C::A_TX + box * 128);
       const int b_row = t.p0 + crank * need;
       const CUtensorMap *mA = &f.tmA[sh], *mB = &f.tmB[sh][bsel];
@@ -798,9 +805,7 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, NB_, EG, SPLI
       } else {
         // 16 columns (tokens) at a time. A warp holds 32 weight rows, one a lane,
         // of each; the outputs want consecutive rows of one token in a thread.
-        // Every warp turns its 32 x 16 block around in a buffer of its own, at
-        // most two warps meeting in a barrier. Thread: 8 rows (part) of token
-        // lane / 4, so that 16-byte stores cover 64 consecutive bytes a token.
+        // Every warp turns its 32 x 16 block around in a buffer of its own.
         const int tok = lane >> 2, part = lane & 3;
         float* bufs = epi + eg * 4 * C::EPI_BUF;
         float* mine_buf = bufs + q * C::EPI_BUF;
@@ -814,7 +819,7 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, NB_, EG, SPLI
             // q + 2 share 32 features, a block of h, which is quantized from
             // fp32; each takes 8 of the tokens.
             const int b = q & 1;
-            named_barrier_sync(2 + eg * 2 + b, 64);
+            named_barrier_sync(4 + eg * 2 + b, 64);
             const int pt = (q >> 1) * 8 + tok;
             const float* gb = bufs + b * C::EPI_BUF + pt * 36 + part * 8;
             const float* ub = gb + 2 * C::EPI_BUF;
@@ -847,23 +852,29 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, NB_, EG, SPLI
                 osc[(((int64_t)t.tb * kt_out + (t.nb >> 1)) * C::RA + (j >> 7)) * 512 +
                     mxfp4_scale_word((uint32_t)(j & 127)) + (t.nb & 1) * 2 + b] = (uint8_t)byte;
             }
-            named_barrier_sync(2 + eg * 2 + b, 64);
+            named_barrier_sync(4 + eg * 2 + b, 64);
           } else {
-            __syncwarp();
+            // All four warps' rows of a token together: a warp takes four tokens,
+            // a thread 8 rows (quarter qq, part) of one, so that its 16-byte store
+            // is part of 256 consecutive bytes (512 for fp32 outputs). Requests
+            // of 64 bytes, a warp's own rows, cost the down GEMM XXX us.
+            named_barrier_sync(2 + eg, 128);
+            const int qq = (lane >> 2) & 3;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              const int pt = i * 8 + tok, j = c0 + pt;
-              const float4* src = reinterpret_cast<const float4*>(mine_buf + pt * 36 + part * 8);
+              const int pt = q * 4 + i * 2 + (lane >> 4), j = c0 + pt;
+              const float4* src =
+                  reinterpret_cast<const float4*>(bufs + qq * C::EPI_BUF + pt * 36 + part * 8);
               const float4 lo = src[0], hi = src[1];
               const float o[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
               if constexpr (MODE == kDownMx4 || FUSED) {
-                // The warp's 32 features are a block of the position's slot row.
+                // Four threads hold a block of 32 features of the slot row.
                 const uint32_t byte = slot_scale_byte(amax_of_four(o));
                 const float inv = mx_inv_scale(byte);
                 if (j < t.n_valid) {
                   const int64_t at = ((int64_t)(shared ? args.T * args.k : 0) + t.p0 + j) *
                                          (f.rows[0] / 32) +
-                                     t.nb * 4 + q;
+                                     t.nb * 4 + qq;
                   reinterpret_cast<uint4*>(f.out)[at * 4 + part] =
                       make_uint4(slot_pair(o[0], o[1], inv), slot_pair(o[2], o[3], inv),
                                  slot_pair(o[4], o[5], inv), slot_pair(o[6], o[7], inv));
@@ -871,11 +882,11 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, NB_, EG, SPLI
                 }
               } else if (j < t.n_valid) {
                 store_outputs(o, f.out, (int64_t)(t.p0 + j) * args.ld_out,
-                              t.nb * 128 + q * 32 + part * 8, f.rows[0], args.out_f32 != 0,
+                              t.nb * 128 + qq * 32 + part * 8, f.rows[0], args.out_f32 != 0,
                               args.vec_out != 0);
               }
             }
-            __syncwarp();
+            named_barrier_sync(2 + eg, 128);
           }
         }
       }
@@ -1010,10 +1021,9 @@ bool set_tokens(Mx4Phase& a, int i, const TokenMaps& t, const Mx4Tiling& tl) {
   a.sB[i] = t.s;
   if (!tl.pairs) return make_tma_map(&a.tmB[i][0], t.q, MOE_DTYPE_E4M3, t.rows, cols, tl.rows);
   using C = Mx4Cfg<kDownMx4, F4, 2, kPairTile, 6, 1, 2, false>;
-  return make_tma_map(&a.tmB[i][0], t.q, MOE_DTYPE_E4M3, t.rows, cols, C::B_ROWS) &&
-         make_tma_map(&a.tmB[i][1], t.q, MOE_DTYPE_E4M3, t.rows, cols, C::BOX1) &&
-         make_tma_map(&a.tmB[i][2], t.q, MOE_DTYPE_E4M3, t.rows, cols, C::BOX2) &&
-         make_scale_tile_map(&a.tmSB[i], t.s, t.tiles * t.kt * C::RA, C::KT_STAGE * C::RA);
+  for (int b = 0; b < 5; ++b)
+    if (!make_tma_map(&a.tmB[i][b], t.q, MOE_DTYPE_E4M3, t.rows, cols, pair_box(b))) return false;
+  return make_scale_tile_map(&a.tmSB[i], t.s, t.tiles * t.kt * C::RA, C::KT_STAGE * C::RA);
 }
 
 template <bool F4>
@@ -1067,7 +1077,7 @@ bool set_phase(Mx4Phase& f, const GemmProblem& p, bool gated, const Mx4Weights& 
   f.tmA[1] = f.tmA[0];
   f.tmSA[1] = f.tmSA[0];
   f.tmSB[1] = f.tmSB[0];
-  for (int i = 0; i < 3; ++i) f.tmB[1][i] = f.tmB[0][i];
+  for (int i = 0; i < 5; ++i) f.tmB[1][i] = f.tmB[0][i];
   return true;
 }
 
