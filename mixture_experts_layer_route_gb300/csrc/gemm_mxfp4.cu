@@ -217,13 +217,18 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int* st
   }
 }
 
-// One unit of work of a CTA (pair): weight row block nb (of 128 rows; pairs
-// take 2 nb and 2 nb + 1) of group g on one token tile, over stages [s0, s1) of
-// the contraction.
+// One unit of work of a CTA (pair): a 128-row block of a group's weights (pairs
+// take blocks 2 n and 2 n + 1) on one token tile.
 struct Mx4Tile {
-  int phase, g, nb, p0, n_valid, s0, s1;
-  int tb;  // scale tile of the token tile
+  int kind;  // columns | shared << 16 | phase << 17
+  int rt;    // 128-row tile of the weights
+  int nb;    // and within the group
+  int p0;    // first position (shared group: token)
+  int tb;    // scale tile of the token tile
 };
+__device__ __forceinline__ int tile_cols(int kind) { return kind & 0xFFFF; }
+__device__ __forceinline__ int tile_shared(int kind) { return (kind >> 16) & 1; }
+__device__ __forceinline__ int tile_phase(int kind) { return kind >> 17; }
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
                                           uint32_t bar, uint64_t policy) {
@@ -516,75 +521,68 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, NB_, EG, SPLI
   }
   auto compute_tile = [&](int u) {
     Mx4Tile t;
-    int m, mt;
+    int m, mt, sh = 0, phase = 0;
     if constexpr (GROUPED) {
-      t.phase = FUSED && u >= units0 ? 1 : 0;
+      phase = FUSED && u >= units0 ? 1 : 0;
       // The two phases' lists hold light groups (decode-sized batches); a single
       // one deals its heavy units evenly among the light ones.
-      u = FUSED ? u - (t.phase ? units0 : 0) : remap_unit(u, total, heavy_units);
+      u = FUSED ? u - (phase ? units0 : 0) : remap_unit(u, total, heavy_units);
       int lo = 0, hi = ngroups;
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (units_before(t.phase, mid) <= u) lo = mid;
+        if (units_before(phase, mid) <= u) lo = mid;
         else hi = mid;
       }
-      const int g = order[lo], local = u - units_before(t.phase, lo);
+      const int g = order[lo], local = u - units_before(phase, lo);
       m = offs[g + 1] - offs[g];
       const int mtiles = (m + BN - 1) / BN;
-      t.g = g;
+      sh = g == E ? 1 : 0;
       t.nb = local / mtiles;  // token tiles fastest: they share weights
       mt = local - t.nb * mtiles;
       t.nb = t.nb * CL + crank;
-      t.tb = g == E ? 0 : (int)group_scale_tile(offs[g], g, BN);
-      t.p0 = g == E ? 0 : offs[g];  // the shared group's rows are in token order
-      t.s0 = 0;
-      t.s1 = (args.ph[t.phase].kt[g == E] + C::KT_STAGE - 1) / C::KT_STAGE;
+      t.rt = (sh ? 0 : g * (args.ph[phase].rows[0] / 128)) + t.nb;
+      t.tb = sh ? 0 : (int)group_scale_tile(offs[g], g, BN);
+      t.p0 = sh ? 0 : offs[g];  // the shared group's rows are in token order
     } else {
       // Token tiles fastest, so that the CTAs at work share weight rows in L2.
       const int lin_mt = (args.T + BN - 1) / BN;
-      t.phase = 0;
-      t.g = 0;
       mt = u % lin_mt;
-      t.nb = u / lin_mt * CL + crank;
+      t.rt = t.nb = u / lin_mt * CL + crank;
       m = args.T;
-      t.tb = 0;
-      t.p0 = 0;
-      const int n = (args.ph[0].kt[0] + C::KT_STAGE - 1) / C::KT_STAGE;
-      const int rank = SPLIT ? (int)cluster_ctarank() : 0;
-      t.s0 = rank * n / splits;  // never empty: splits <= n
-      t.s1 = (rank + 1) * n / splits;
+      t.tb = t.p0 = 0;
     }
     const int tn = token_tile_rows(m, BN, C::N_UNIT);
     t.tb += mt;
     t.p0 += mt * tn;
-    t.n_valid = min(tn, m - mt * tn);
+    t.kind = min(tn, m - mt * tn) | sh << 16 | phase << 17;
     return t;
   };
-  // The tile of this CTA's unit number lt (unit cid + lt ncl). A warp computes 32
-  // units at a time, one a lane (the searches and divisions take ~600 cycles),
-  // and hands each out as a warp-uniform value.
+  // A warp computes its next 32 units at a time, one a lane (the searches and
+  // divisions take ~600 cycles), and hands each one's fields out as warp-uniform
+  // values. The roles fetch a unit's in the middle of the one before, not between
+  // the two (prompt chunk: gate/up 495 -> 489 us, down 350 -> 340 us).
   Mx4Tile mine = {};
-  auto tile_at = [&](int lt) {
+  auto refresh = [&](int lt) {
     if ((lt & 31) == 0) {
       const int64_t u = cid + (int64_t)(lt + lane) * ncl;
       if (u < total) mine = compute_tile((int)u);
       __syncwarp();
     }
-    const int src = lt & 31;
-    Mx4Tile t;
-    t.phase = FUSED ? uniform(__shfl_sync(0xffffffffu, mine.phase, src)) : 0;
-    t.g = uniform(__shfl_sync(0xffffffffu, mine.g, src));
-    t.nb = uniform(__shfl_sync(0xffffffffu, mine.nb, src));
-    t.p0 = uniform(__shfl_sync(0xffffffffu, mine.p0, src));
-    t.n_valid = uniform(__shfl_sync(0xffffffffu, mine.n_valid, src));
-    t.tb = uniform(__shfl_sync(0xffffffffu, mine.tb, src));
-    t.s0 = uniform(__shfl_sync(0xffffffffu, mine.s0, src));
-    t.s1 = uniform(__shfl_sync(0xffffffffu, mine.s1, src));
-    return t;
+  };
+  auto pick = [&](int field, int lt) {
+    return uniform(__shfl_sync(0xffffffffu, field, lt & 31));
   };
   const int n_units = total > cid ? (total - cid + ncl - 1) / ncl : 0;  // of this CTA
-  auto mma_cols = [&](const Mx4Tile& t) {
-    return (t.n_valid + C::N_UNIT - 1) / C::N_UNIT * C::N_UNIT;
+  // Stages [s0, s1) of the contraction that this CTA takes of a unit.
+  auto stage_range = [&](int kind, int* s0, int* s1) {
+    const int n =
+        (args.ph[tile_phase(kind)].kt[tile_shared(kind)] + C::KT_STAGE - 1) / C::KT_STAGE;
+    const int rank = SPLIT ? (int)cluster_ctarank() : 0;
+    *s0 = rank * n / splits;  // never empty: splits <= n
+    *s1 = (rank + 1) * n / splits;
+  };
+  auto mma_cols = [&](int kind) {
+    return (tile_cols(kind) + C::N_UNIT - 1) / C::N_UNIT * C::N_UNIT;
   };
 
   if (warp == 0) {
@@ -604,11 +602,15 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, NB_, EG, SPLI
       else
         tma_load_2d(dst, m, x, y, bar(b), pol);
     };
-    auto row_block_of = [&](const Mx4Tile& t, int sh) {
-      return (sh || !GROUPED ? 0 : t.g * (args.ph[t.phase].rows[0] / 128)) + t.nb;
-    };
     Mx4Tile next = {};
-    if (n_units > 0) next = tile_at(0);
+    auto fetch = [&](int lt) {
+      refresh(lt);
+      next.kind = pick(mine.kind, lt);
+      next.rt = pick(mine.rt, lt);
+      next.p0 = pick(mine.p0, lt);
+      next.tb = pick(mine.tb, lt);
+    };
+    if (n_units > 0) fetch(0);
     // Test hook: the first stage is neither signalled nor loaded, so that the
     // MMA issuer's wait on it runs out.
     const int skip = (args.flags & MOE_FLAG_TEST_SKIP_SIGNAL) != 0 ? 1 : 0;
@@ -620,13 +622,13 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, NB_, EG, SPLI
     bool peek = false;
     for (int lt = 0; lt < n_units && ok; ++lt) {
       const Mx4Tile t = next;
-      const Mx4Phase& f = args.ph[t.phase];
-      const int sh = GROUPED && t.g == E ? 1 : 0;
+      const int phase = FUSED ? tile_phase(t.kind) : 0, sh = GROUPED ? tile_shared(t.kind) : 0;
+      const Mx4Phase& f = args.ph[phase];
       const int kt = f.kt[sh];
       // The last row block of a pair may lie past the group's rows: it loads
       // what is there (another group's rows, or zeros) and stores nothing.
-      const int rt = row_block_of(t, sh);
-      const int need = mma_cols(t) / CL;
+      const int rt = t.rt;
+      const int need = mma_cols(t.kind) / CL;
       int bsel = 0;
       if constexpr (PAIR) bsel = need > 96 ? 0 : (need > 80 ? 1 : (need > 64 ? 2 : (need > 32 ? 3 : 4)));
       const int box = PAIR ? pair_box(bsel) : C::B_ROWS;
@@ -634,13 +636,13 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, NB_, EG, SPLI
       const int b_row = t.p0 + crank * need;
       const CUtensorMap *mA = &f.tmA[sh], *mB = &f.tmB[sh][bsel];
       const int sa_row = rt * kt, sb_row = t.tb * kt * C::RA;
-      const int s0 = t.s0, s1 = t.s1;
-      if (lt + 1 < n_units) next = tile_at(lt + 1);
+      int s0, s1;
+      stage_range(t.kind, &s0, &s1);
       if constexpr (FUSED) {
         // A down unit reads h rows that other CTAs wrote: all row blocks of this
         // token tile's gate/up product have to be done. Those units come before
         // any down unit in every CTA's list, and all CTAs are resident.
-        if (t.phase == 1) {
+        if (phase == 1) {
           int there = 1;
           if (el) {
             const int need = args.ph[0].rows[sh] / 128;
@@ -681,7 +683,9 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, NB_, EG, SPLI
         }
         ++it;
         if (++s == STAGES) s = 0, ph ^= 1u;
+        if (st == s0 && lt + 1 < n_units) fetch(lt + 1);
       }
+      if (first && lt + 1 < n_units) fetch(lt + 1);  // the loop began past s0
       first = 0;
     }
     // Let the last loads land before the CTA (pair) can exit.
@@ -708,18 +712,22 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, NB_, EG, SPLI
       int s = 0;
       uint32_t ph = 0, par = 0;
       bool ok = true, peek = false;
-      Mx4Tile next = {};
-      if (n_units > 0) next = tile_at(0);
+      int next = 0;
+      if (n_units > 0) {
+        refresh(0);
+        next = pick(mine.kind, 0);
+      }
       for (int lt = 0; lt < n_units && ok; ++lt) {
-        const Mx4Tile t = next;
-        const int kt = args.ph[t.phase].kt[GROUPED && t.g == E ? 1 : 0];
-        const int s0 = t.s0, s1 = t.s1;
+        const int kind = next;
+        const int kt = args.ph[FUSED ? tile_phase(kind) : 0].kt[GROUPED ? tile_shared(kind) : 0];
+        int s0, s1;
+        stage_range(kind, &s0, &s1);
         const uint32_t acc = lt & 1u;
         if (!(ok = warp_wait(tempty_bar(acc), ((lt >> 1) & 1u) ^ 1u, args.status, limit))) break;
         tc_fence_after();
         const uint32_t d = tmem_base + acc * BN;
         const uint32_t idesc = idesc_scaled(F4 ? 1 : 5, F4 ? 1 : 0, 128 * CL,
-                                            (uint32_t)mma_cols(t), 0);
+                                            (uint32_t)mma_cols(kind), 0);
         uint32_t accumulate = 0;
         for (int st = s0; st < s1; ++st) {
           if (!(ok = warp_wait(full_bar(s), ph, args.status, limit, peek))) break;
@@ -759,12 +767,15 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, NB_, EG, SPLI
           __syncwarp();
           accumulate = 1;
           par ^= C::NB & 1u;
+          if (st == s0 && lt + 1 < n_units) {
+            refresh(lt + 1);
+            next = pick(mine.kind, lt + 1);
+          }
           if (++s == STAGES) s = 0, ph ^= 1u;
         }
         if (!ok) break;
         if (el) commit(tfull_bar(acc));
         __syncwarp();
-        if (lt + 1 < n_units) next = tile_at(lt + 1);
       }
       if (el) {
         if constexpr (PAIR)
@@ -782,21 +793,24 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, NB_, EG, SPLI
     const int et = threadIdx.x - 64;      // 0..EPI_THREADS-1
     const uint32_t lane_base = (uint32_t)(q * 32) << 16;
     for (int lt = 0; lt < n_units; ++lt) {
-      const Mx4Tile t = tile_at(lt);
-      const bool shared = GROUPED && t.g == E;
+      refresh(lt);
+      const int kind = pick(mine.kind, lt), t_nb = pick(mine.nb, lt), t_p0 = pick(mine.p0, lt),
+                t_tb = pick(mine.tb, lt);
+      const bool shared = GROUPED && tile_shared(kind);
+      const int n_valid = tile_cols(kind), phase = FUSED ? tile_phase(kind) : 0;
       const uint32_t acc = lt & 1u;
       if (et == 0) *epi_flag = mbar_wait(tfull_bar(acc), (lt >> 1) & 1u, args.status, limit) ? 1 : 0;
       named_barrier_sync(1, C::EPI_THREADS);
       if (!*epi_flag) break;  // every epilogue thread sees the same flag
       tc_fence_after();
       const uint32_t t_acc = tmem_base + lane_base + acc * BN;
-      const Mx4Phase& f = args.ph[t.phase];
-      const bool live = t.nb * 128 < f.rows[shared];  // a pair's block past the last one
+      const Mx4Phase& f = args.ph[phase];
+      const bool live = t_nb * 128 < f.rows[shared];  // a pair's block past the last one
       if constexpr (SPLIT) {
         // Partial sums to shared memory ([column][row], over the drained ring);
         // the cluster adds them below.
         float* part = reinterpret_cast<float*>(stages);
-        for (int c0 = 32 * eg; c0 < t.n_valid; c0 += 32 * EG) {
+        for (int c0 = 32 * eg; c0 < n_valid; c0 += 32 * EG) {
           float v[32];
           tmem_ld32(t_acc + c0, v);
 #pragma unroll
@@ -809,12 +823,12 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, NB_, EG, SPLI
         const int tok = lane >> 2, part = lane & 3;
         float* bufs = epi + eg * 4 * C::EPI_BUF;
         float* mine_buf = bufs + q * C::EPI_BUF;
-        for (int c0 = 16 * eg; live && c0 < t.n_valid; c0 += 16 * EG) {
+        for (int c0 = 16 * eg; live && c0 < n_valid; c0 += 16 * EG) {
           float v[16];
           tmem_ld16(t_acc + c0, v);
 #pragma unroll
           for (int i = 0; i < 16; ++i) mine_buf[i * 36 + lane] = v[i];
-          if (MODE == kGatedMx4 || (FUSED && t.phase == 0)) {
+          if (MODE == kGatedMx4 || (FUSED && phase == 0)) {
             // Rows 0..63 are gate, 64..127 up, of features 64 nb ..: warps q and
             // q + 2 share 32 features, a block of h, which is quantized from
             // fp32; each takes 8 of the tokens.
@@ -838,19 +852,19 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, NB_, EG, SPLI
             const uint32_t byte = mx_scale_byte(amax_of_four(hv), 8);
             const float inv = mx_inv_scale(byte);
             const int j = c0 + pt;
-            if (j < t.n_valid) {
+            if (j < n_valid) {
               const int kt_out = f.rows[shared] / 256;  // I / 128
               uint8_t* out = reinterpret_cast<uint8_t*>(shared ? f.out_shared : f.out);
               uint8_t* osc = shared ? f.out_shared_s : f.out_s;
               uint2 codes = make_uint2(mx_encode4(hv[0] * inv, hv[1] * inv, hv[2] * inv, hv[3] * inv),
                                        mx_encode4(hv[4] * inv, hv[5] * inv, hv[6] * inv, hv[7] * inv));
               if (byte == 255u) codes = make_uint2(0, 0);  // a NaN block
-              *reinterpret_cast<uint2*>(out + (size_t)(t.p0 + j) * (kt_out * 128) + t.nb * 64 +
+              *reinterpret_cast<uint2*>(out + (size_t)(t_p0 + j) * (kt_out * 128) + t_nb * 64 +
                                         b * 32 + part * 8) = codes;
               // Features 64 nb: k tile nb / 2, blocks 0,1 or 2,3 of it.
               if (part == 0)
-                osc[(((int64_t)t.tb * kt_out + (t.nb >> 1)) * C::RA + (j >> 7)) * 512 +
-                    mxfp4_scale_word((uint32_t)(j & 127)) + (t.nb & 1) * 2 + b] = (uint8_t)byte;
+                osc[(((int64_t)t_tb * kt_out + (t_nb >> 1)) * C::RA + (j >> 7)) * 512 +
+                    mxfp4_scale_word((uint32_t)(j & 127)) + (t_nb & 1) * 2 + b] = (uint8_t)byte;
             }
             named_barrier_sync(4 + eg * 2 + b, 64);
           } else {
@@ -871,18 +885,18 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, NB_, EG, SPLI
                 // Four threads hold a block of 32 features of the slot row.
                 const uint32_t byte = slot_scale_byte(amax_of_four(o));
                 const float inv = mx_inv_scale(byte);
-                if (j < t.n_valid) {
-                  const int64_t at = ((int64_t)(shared ? args.T * args.k : 0) + t.p0 + j) *
+                if (j < n_valid) {
+                  const int64_t at = ((int64_t)(shared ? args.T * args.k : 0) + t_p0 + j) *
                                          (f.rows[0] / 32) +
-                                     t.nb * 4 + qq;
+                                     t_nb * 4 + qq;
                   reinterpret_cast<uint4*>(f.out)[at * 4 + part] =
                       make_uint4(slot_pair(o[0], o[1], inv), slot_pair(o[2], o[3], inv),
                                  slot_pair(o[4], o[5], inv), slot_pair(o[6], o[7], inv));
                   if (part == 0) f.out_s[at] = (uint8_t)byte;
                 }
-              } else if (j < t.n_valid) {
-                store_outputs(o, f.out, (int64_t)(t.p0 + j) * args.ld_out,
-                              t.nb * 128 + qq * 32 + part * 8, f.rows[0], args.out_f32 != 0,
+              } else if (j < n_valid) {
+                store_outputs(o, f.out, (int64_t)(t_p0 + j) * args.ld_out,
+                              t_nb * 128 + qq * 32 + part * 8, f.rows[0], args.out_f32 != 0,
                               args.vec_out != 0);
               }
             }
@@ -902,12 +916,12 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, NB_, EG, SPLI
       if constexpr (FUSED) {
         // This unit's h rows, stored by every epilogue thread, become visible at
         // GPU scope and to the async proxy before the tile's count moves.
-        if (t.phase == 0) {
+        if (phase == 0) {
           fence_proxy_async_global();
           __threadfence();
           named_barrier_sync(1, C::EPI_THREADS);
           if (et == 0)
-            red_release_gpu_add(args.done + (shared ? args.done_shared : 0) + t.tb, 1);
+            red_release_gpu_add(args.done + (shared ? args.done_shared : 0) + t_tb, 1);
         }
       }
     }
@@ -922,7 +936,7 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, NB_, EG, SPLI
     // Each CTA adds its share of the tile's outputs over the cluster's partial
     // sums, in the order of K.
     const Mx4Tile t = compute_tile(cid);
-    const int quads = t.n_valid * 32;  // 4 rows of one column each
+    const int quads = tile_cols(t.kind) * 32;  // 4 rows of one column each
     const int per = (quads + splits - 1) / splits;
     const int q0 = (int)cluster_ctarank() * per, q1 = min(quads, q0 + per);
     for (int i = q0 + (int)threadIdx.x; i < q1; i += C::THREADS) {
