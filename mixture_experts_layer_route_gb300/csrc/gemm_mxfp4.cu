@@ -30,9 +30,11 @@
 //    elected lane issuing, and every loop bound comes through a warp
 //    reduction, so that the operands are provably warp-uniform (a loop under
 //    `lane == 0` took 85 cycles per MMA and 130 per scale copy);
-//  - NB = 2: one wait and one commit for eight MMAs. One box a stage took 460
-//    cycles on the decode layer's gate/up GEMM, where HBM delivers its 8 KB in
-//    350.
+//  - single CTAs take NB = 2 boxes a stage: one wait and one commit for eight
+//    MMAs. One box a stage took 460 cycles on the decode layer's gate/up GEMM,
+//    where HBM delivers its 8 KB in 350. Pairs, whose MMAs take longer (N up to
+//    224), take six stages of one box instead of three of two: the ring then
+//    refills in smaller steps (prompt chunk: down 357 -> 349 us).
 //
 // Warp roles: warp 0 TMA producer, warp 1 MMA issuer (one thread) and owner of
 // the tensor memory, the others epilogue (four per group, one 32-lane quarter
@@ -112,7 +114,6 @@ struct Mx4Cfg {
   static constexpr int SF_COLS = KT_BOX * 4 * (1 + RA);
   static constexpr int USED_COLS = 2 * BN + 2 * SF_COLS;
   static constexpr int TMEM_COLS = USED_COLS <= 128 ? 128 : (USED_COLS <= 256 ? 256 : 512);
-  static constexpr int EPI_GROUPS = EG;
   static constexpr int EPI_THREADS = 128 * EG;
   static constexpr int THREADS = 64 + EPI_THREADS;
   // Floats per epilogue warp: 16 tokens x 32 rows, padded so that eight lanes
@@ -126,7 +127,8 @@ struct Mx4Cfg {
   static_assert(STAGE_BYTES % 1024 == 0 && B_BOX % 1024 == 0, "swizzled boxes start on 1 KB");
 
   static size_t smem_bytes(int E) {
-    return 1024 + (size_t)STAGES * STAGE_BYTES + EPI_FLOATS * 4 + NBARS * 8 + 32 + (MODE == kLinearMx4 ? 0 : 3 * (size_t)(E + 2) * 4);
+    return 1024 + (size_t)STAGES * STAGE_BYTES + EPI_FLOATS * 4 + NBARS * 8 + 32 +
+           (MODE == kLinearMx4 ? 0 : 3 * (size_t)(E + 2) * 4);
   }
 };
 
@@ -426,9 +428,10 @@ __device__ __forceinline__ void build_schedule_block(const Mx4Args& a, int tile_
 template <int MODE, bool F4, int CL, int BN, int STAGES, int NB_, int EG, bool SPLIT>
 __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, NB_, EG, SPLIT>::THREADS, 1)
     mx4_gemm_kernel(const __grid_constant__ Mx4Args args) {
-  pdl_trigger();
   using C = Mx4Cfg<MODE, F4, CL, BN, STAGES, NB_, EG, SPLIT>;
   constexpr bool PAIR = CL == 2;
+  // Pairs share the GPU with no other kernel (launch_variant).
+  if constexpr (!PAIR) pdl_trigger();
   constexpr bool GROUPED = MODE != kLinearMx4, FUSED = MODE == kExpertsMx4;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -870,8 +873,9 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, NB_, EG, SPLI
           } else {
             // All four warps' rows of a token together: a warp takes four tokens,
             // a thread 8 rows (quarter qq, part) of one, so that its 16-byte store
-            // is part of 256 consecutive bytes (512 for fp32 outputs). Requests
-            // of 64 bytes, a warp's own rows, cost the down GEMM XXX us.
+            // is part of 256 consecutive bytes (512 for fp32 outputs; a prompt
+            // chunk's down GEMM: 349 us, 357 us with requests of 64 bytes, a
+            // warp's own rows).
             named_barrier_sync(2 + eg, 128);
             const int qq = (lane >> 2) & 3;
 #pragma unroll
@@ -927,6 +931,7 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, NB_, EG, SPLI
     }
   }
 
+  __syncwarp();
   tc_fence_before();
   if constexpr (PAIR || SPLIT)
     cluster_sync();
@@ -960,10 +965,38 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, NB_, EG, SPLI
     else
       tmem_dealloc(tmem_base, C::TMEM_COLS);
   }
+  if constexpr (PAIR) cluster_sync();  // neither CTA leaves before both have freed theirs
 }
 
 constexpr int kMaxExperts = 1024;  // the C ABI's limit on E
 constexpr int kPairTile = 224;
+
+// A launch of CTA pairs in plain stream order, without programmatic dependence on
+// either side, so that no other kernel's CTAs start or wait on the SMs of a pair.
+// Chained like the other kernels, products of a few us that followed each other in
+// a graph stopped making progress (three times in some thousand replays of 20; every
+// wait inside the kernel is bounded, and reading found no cause); launched like this
+// they ran 4800 replays. It is no slower: with its quantization, 8192 x 4096 x 4096
+// takes 91 us (chained 97), with E2M1 tokens 60 us (65), as the next call's blocks no
+// longer share the SMs; 512 x 8192 x 2048 takes 12.7 us.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_alone(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                         cudaStream_t st, unsigned cluster_x, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster_x;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
 
 template <int MODE, bool F4, int CL, int BN, int STAGES, int NB_, int EG, bool SPLIT>
 cudaError_t launch_variant(const Mx4Args& a, int num_sms, size_t units, int splits,
@@ -977,8 +1010,10 @@ cudaError_t launch_variant(const Mx4Args& a, int num_sms, size_t units, int spli
   size_t n = (size_t)(num_sms / CL);
   if (SPLIT || units < n) n = units;  // a split tile is one cluster's only unit
   const size_t cluster = (size_t)(CL * (SPLIT ? splits : 1));
-  return launch_chained(fn, dim3((unsigned)(n * cluster)), dim3(C::THREADS), C::smem_bytes(a.E),
-                        st, (unsigned)cluster, a);
+  const dim3 grid((unsigned)(n * cluster));
+  if constexpr (CL == 2)
+    return launch_alone(fn, grid, dim3(C::THREADS), C::smem_bytes(a.E), st, (unsigned)cluster, a);
+  return launch_chained(fn, grid, dim3(C::THREADS), C::smem_bytes(a.E), st, (unsigned)cluster, a);
 }
 
 // A launch whose blocks are all resident at once, chained to its predecessor.
@@ -1001,10 +1036,20 @@ cudaError_t launch_cooperative(void (*kernel)(KArgs...), dim3 grid, dim3 block, 
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+template <int BN>
+cudaError_t launch_experts_variant(const Mx4Args& a, size_t ctas, cudaStream_t st) {
+  using C = Mx4Cfg<kExpertsMx4, false, 1, BN, 4, 2, 1, false>;
+  auto fn = mx4_gemm_kernel<kExpertsMx4, false, 1, BN, 4, 2, 1, false>;
+  cudaError_t e = ensure_smem_attr((const void*)fn, C::smem_bytes(kMaxExperts));
+  if (e != cudaSuccess || ctas == 0) return e;
+  return launch_cooperative(fn, dim3((unsigned)ctas), dim3(C::THREADS), C::smem_bytes(a.E), st, a);
+}
+
 // Token tiles: 32 or 64 rows on single CTAs (4 stages of 42 to 52 KB), 224 rows
-// on pairs (3 stages of 63 or 66 KB; two accumulators of 224 columns and the
-// scales fill tensor memory; two epilogue groups). The layer's single-CTA tiles
-// run in launch_mx4_experts.
+// on pairs (6 stages of 32 or 33 KB; two accumulators of 224 columns and the
+// scales fill tensor memory; two epilogue groups: with one, a prompt chunk's down
+// GEMM took 441 us instead of 345). The layer's single-CTA tiles run in
+// launch_mx4_experts.
 template <int MODE, bool F4>
 cudaError_t launch_mx4(const Mx4Args& a, const Mx4Tiling& t, int num_sms, size_t units, int splits,
                        cudaStream_t st) {
@@ -1053,11 +1098,21 @@ bool set_weights(Mx4Phase& a, int i, const uint8_t* q, const uint8_t* s, uint64_
 
 }  // namespace
 
-// Grouped products: 32-row tiles up to 64 tokens (or when forced), pairs above.
+// Grouped products: single CTAs on tiles of 32 rows up to 64 tokens and of 64 rows
+// up to 512 (both GEMMs in one launch), pairs above; or what `tile` asks for. The
+// layer's time in us by tokens, 32 / 64 rows / pairs (k of E experts,
+// H x I, loads even or by Zipf's law with exponent 1.1):
+//                              T = 8          64           256          512          1024
+//   8 of 128, 4096x1536   100/116/125  211/214/254  230/234/274  308/258/294  462/338/331
+//     Zipf                 74/82/95    126/123/152  221/198/225  332/279/275  506/383/346
+//   10 of 512, 4096x1024  109/112/137  390/395/463  573/579/666  601/607/690  636/638/727
+//     Zipf                 74/75/96    126/123/154  229/209/238  328/284/298  513/419/399
+//   2 of 8, 4096x2048      44/56/53     44/44/57     62/53/64     85/63/71    143/99/96
 Mx4Tiling mx4_tiling(int64_t T, int tile) {
-  const bool pairs = tile == MOE_TILE_MEDIUM || tile == MOE_TILE_PREFILL ||
-                     (tile == MOE_TILE_AUTO && T > 64);
-  return pairs ? Mx4Tiling{true, kPairTile, 32, 2} : Mx4Tiling{false, 32, 16, 1};
+  if (tile == MOE_TILE_AUTO)
+    tile = T <= 64 ? MOE_TILE_DECODE : (T <= 512 ? MOE_TILE_MEDIUM : MOE_TILE_PREFILL);
+  if (tile == MOE_TILE_PREFILL) return {true, kPairTile, 32, 2};
+  return {false, tile == MOE_TILE_MEDIUM ? 64 : 32, 16, 1};
 }
 
 namespace {
@@ -1160,29 +1215,34 @@ cudaError_t launch_mx4_experts(const GemmProblem& p, const Mx4Weights& w, const 
   set_problem(a, p, offsets, status);
   a.done = done;
   a.done_shared = (int)group_scale_tile((int64_t)p.T * p.k, p.E, tl.rows) + 1;
-  using C = Mx4Cfg<kExpertsMx4, false, 1, 32, 4, 2, 1, false>;
-  auto fn = mx4_gemm_kernel<kExpertsMx4, false, 1, 32, 4, 2, 1, false>;
-  cudaError_t e = ensure_smem_attr((const void*)fn, C::smem_bytes(kMaxExperts));
-  if (e != cudaSuccess) return e;
   size_t n = phase_units(p, a.ph[0], tl) + phase_units(p, a.ph[1], tl);
   if (n > (size_t)p.num_sms) n = (size_t)p.num_sms;
-  if (n == 0) return cudaSuccess;
-  return launch_cooperative(fn, dim3((unsigned)n), dim3(C::THREADS), C::smem_bytes(a.E), st, a);
+  return tl.rows == 32 ? launch_experts_variant<32>(a, n, st)
+                       : launch_experts_variant<64>(a, n, st);
 }
 
 // Tiling and clusters over K of a dense product.
 Mx4LinearPlan mx4_linear_plan(int64_t T, int64_t N, int64_t K, int num_sms) {
   const int64_t kt = mxfp4_k_tiles(K);
   const int64_t blocks = (N + 127) / 128;
-  // Pairs when they fill at least half of the GPU.
+  // Pairs when they fill at least half of the GPU (mxfp8, 16384 x 7168: T = 128,
+  // 16.8 us on pairs, 24.9 us on 64-row tiles; 4096 x 4096, T = 256 on 32 pairs,
+  // 12.0 us, 11.4 us).
   const int64_t pair_units = (blocks + 1) / 2 * ((T + kPairTile - 1) / kPairTile);
   if (T > 64 && pair_units * 4 >= num_sms) return {{true, kPairTile, 32, 2}, 1};
+  // 64-row tiles stream the weights once for up to 64 tokens (16384 x 7168, T = 48:
+  // 15.5 us, 22.2 us as two tiles of 32); 32 rows leave room for deeper stages'
+  // worth of weights (T = 16: 14.7 us, 21.6 us with 64).
   const int rows = T <= 32 ? 32 : 64;
   const int64_t units = blocks * ((T + rows - 1) / rows);
   // As many CTAs per tile as still fit the GPU at once and leave each at least
-  // 1024 of K (two to four stages).
+  // 1024 of K (two to four stages): 4096 x 4096, T = 1, 6.7 us in clusters of
+  // four, 8.6 us unsplit. Eight only up to two thirds of the GPU: 12 clusters of
+  // eight run at once (1536 x 8192, T = 1: 6.4 us, 7.3 us in fours), 16 do not
+  // (2048 x 8192: 10.7 us, 7.2 us in fours).
   int splits = 1;
-  while (splits < 8 && units * splits * 2 <= num_sms && kt >= 16 * splits) splits *= 2;
+  while (splits < 8 && units * splits * (splits == 4 ? 3 : 2) <= num_sms && kt >= 16 * splits)
+    splits *= 2;
   return {{false, rows, 16, 1}, splits};
 }
 

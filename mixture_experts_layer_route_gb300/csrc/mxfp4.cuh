@@ -71,11 +71,6 @@ __device__ __forceinline__ float mx_inv_scale(uint32_t byte) {
   return byte == 255u ? 0.0f : __uint_as_float((254u - byte) << 23);
 }
 
-// v * inv, with the elements of a NaN block (inv = 0) as zeros.
-__device__ __forceinline__ float mx_scaled(float v, float inv) {
-  return inv == 0.0f ? 0.0f : v * inv;
-}
-
 // The slots between the down projection and the combine: per position and 32
 // features a scale 2^(byte - 127) and int16 codes v / scale, scale =
 // 2^(floor(log2 a) - 13) for the block's largest magnitude a: |code| <= 2^14
