@@ -1,0 +1,125 @@
+"""A decoder block's MXFP4 products, as a server runs them.
+
+The block projects its input (a dense product with MXFP4 weights and MXFP8
+activations), adds the residual, runs a Mixture-of-Experts layer with MXFP4
+expert weights on the normalised sum, adds that, and projects to logits (a
+dense product with both operands in MXFP4). The weights are quantized once when
+the block is built; a prompt chunk then runs eagerly and a decode step as a CUDA
+graph.
+
+    python examples/mxfp4_block.py [--tokens 2048] [--steps 50]
+"""
+import argparse
+import os
+import sys
+
+import torch
+
+sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+import mixture_experts_layer_route_gb300 as moe  # noqa: E402
+
+
+def norm(x):
+    v = x.float()
+    return (v * torch.rsqrt(v.square().mean(-1, keepdim=True) + 1e-6)).to(x.dtype)
+
+
+class Block:
+    """Projection -> MoE layer -> logits, every weight in MXFP4."""
+
+    def __init__(self, W_in, W_router, W_gate, W_up, W_down, W_out, k):
+        self.project = moe.LinearMXFP4(W_in, act="mxfp8")
+        self.experts = moe.MoELayerMXFP4(W_router, W_gate, W_up, W_down, k)
+        self.logits = moe.LinearMXFP4(W_out, act="mxfp4")
+
+    def __call__(self, x):
+        x = x + self.project(norm(x))
+        x = x + self.experts(norm(x))
+        return self.logits(norm(x), out_f32=True)
+
+
+class PlainBlock:
+    """The same block in fp32 on the values that the quantized weights stand for
+    (expert by expert), with unquantized activations."""
+
+    def __init__(self, W_in, W_router, W_gate, W_up, W_down, W_out, k):
+        def back(W):
+            q, s = moe.quantize_mxfp4_rows(W)
+            cols = W.shape[-1]
+            return moe.dequantize_mxfp4_rows(q, s, W.numel() // cols, cols,
+                                             dtype=torch.float32).view(W.shape)
+        self.W_in, self.W_out = back(W_in), back(W_out)
+        self.gate, self.up, self.down = back(W_gate), back(W_up), back(W_down)
+        self.W_router, self.k = W_router.float(), k
+
+    def moe(self, x):
+        top, ids = (x @ self.W_router.T).topk(self.k, dim=1)
+        w = top.softmax(1)
+        y = torch.zeros_like(x)
+        for e in range(self.gate.shape[0]):
+            t, r = (ids == e).nonzero(as_tuple=True)
+            h = torch.nn.functional.silu(x[t] @ self.gate[e].T) * (x[t] @ self.up[e].T)
+            y.index_add_(0, t, (h @ self.down[e].T) * w[t, r, None])
+        return y
+
+    def __call__(self, x):
+        x = x.float()
+        x = x + norm(x) @ self.W_in.T
+        x = x + self.moe(norm(x))
+        return norm(x) @ self.W_out.T
+
+
+def weights(H, E, I, V, seed=0, device="cuda"):
+    g = torch.Generator(device=device).manual_seed(seed)
+
+    def w(*shape):
+        return (torch.randn(*shape, generator=g, device=device) / shape[-1] ** 0.5).to(torch.bfloat16)
+    return w(H, H), w(E, H), w(E, I, H), w(E, I, H), w(E, H, I), w(V, H)
+
+
+def step_graph(block, x):
+    """A CUDA graph of block(x), and the tensor that its replays write."""
+    block(x)  # workspaces exist before the capture
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = block(x)
+    return graph, y
+
+
+def timed(fn, n):
+    start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    for _ in range(3):
+        fn()
+    start.record()
+    for _ in range(n):
+        fn()
+    end.record()
+    end.synchronize()
+    return start.elapsed_time(end) / n
+
+
+def main():
+    ap = argparse.ArgumentParser(description=__doc__.splitlines()[0])
+    ap.add_argument("--hidden", type=int, default=2048)
+    ap.add_argument("--experts", type=int, default=64)
+    ap.add_argument("--inner", type=int, default=1024)
+    ap.add_argument("--vocab", type=int, default=32000)
+    ap.add_argument("-k", type=int, default=8)
+    ap.add_argument("--tokens", type=int, default=2048, help="tokens of the prompt chunk")
+    ap.add_argument("--batch", type=int, default=16, help="sequences of a decode step")
+    ap.add_argument("--steps", type=int, default=50)
+    a = ap.parse_args()
+    ws = weights(a.hidden, a.experts, a.inner, a.vocab)
+    block, plain = Block(*ws, a.k), PlainBlock(*ws, a.k)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(a.tokens, a.hidden, generator=g, device="cuda").to(torch.bfloat16)
+    y, want = block(x), plain(x)
+    print(f"prompt chunk of {a.tokens}: {timed(lambda: block(x), 10) * 1e3:.0f} us, logits within "
+          f"{float((y - want).norm() / want.norm()):.3f} of unquantized activations")
+    graph, _ = step_graph(block, x[:a.batch].contiguous())
+    print(f"decode step of {a.batch}: {timed(graph.replay, a.steps) * 1e3:.1f} us")
+
+
+if __name__ == "__main__":
+    main()

@@ -343,3 +343,24 @@ def test_layer_at_the_tilings_borders(T):
     d, lay = _layer(cfg, seed=T)
     _close(lay(d["x"], out_f32=True), _reference(cfg, d)[0])
     assert m.get_device_status(lay.workspace(T)) == m.MOE_OK
+
+
+def test_example_block():
+    """The operators together: the example's block against its plain form. The
+    logits differ by the activations' rounding alone: E4M3 in two products (2%
+    of a value at most, and of random sign), E2M1 in the last (a third of a step
+    of 1/2 around a mean of 1: 10 to 15%)."""
+    from examples import mxfp4_block as ex
+    ws = ex.weights(H=256, E=8, I=128, V=500)
+    block, plain = ex.Block(*ws, 2), ex.PlainBlock(*ws, 2)
+    g = torch.Generator(device=DEV).manual_seed(1)
+    for T in (1, 20, 700):
+        x = torch.randn(T, 256, generator=g, device=DEV).to(torch.bfloat16)
+        y, want = block(x), plain(x)
+        assert y.shape == (T, 500) and y.dtype == torch.float32
+        assert (y - want).norm() <= 0.2 * want.norm()
+        graph, out = ex.step_graph(block, x)
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, y)
