@@ -90,7 +90,11 @@ typedef enum {
  * uses 32-token tiles (its rows gathered inside the GEMM's loads); larger
  * batches use tiles of up to 256 tokens on pairs of SMs, all experts in one
  * launch, heaviest first, each tile loading only as many token rows as it
- * holds. DECODE, MEDIUM and PREFILL force 32-, 128- or 256-token tiles. */
+ * holds. DECODE, MEDIUM and PREFILL force 32-, 128- or 256-token tiles.
+ * Layers with MXFP4 weights (moe_forward_mxfp4): AUTO takes 32-token tiles for
+ * T <= 64, 64-token tiles for T <= 512 (both with the two expert GEMMs in one
+ * launch) and tiles of up to 128 or 224 tokens on pairs of SMs above; DECODE, MEDIUM
+ * and PREFILL force these three. */
 typedef enum {
   MOE_TILE_AUTO = 0,
   MOE_TILE_DECODE = 1,

@@ -969,7 +969,7 @@ __global__ void __launch_bounds__(Mx4Cfg<MODE, F4, CL, BN, STAGES, NB_, EG, SPLI
 }
 
 constexpr int kMaxExperts = 1024;  // the C ABI's limit on E
-constexpr int kPairTile = 224;
+constexpr int kPairTile = 224, kSmallPairTile = 128;
 
 // A launch of CTA pairs in plain stream order, without programmatic dependence on
 // either side, so that no other kernel's CTAs start or wait on the SMs of a pair.
@@ -1045,23 +1045,26 @@ cudaError_t launch_experts_variant(const Mx4Args& a, size_t ctas, cudaStream_t s
   return launch_cooperative(fn, dim3((unsigned)ctas), dim3(C::THREADS), C::smem_bytes(a.E), st, a);
 }
 
-// Token tiles: 32 or 64 rows on single CTAs (4 stages of 42 to 52 KB), 224 rows
-// on pairs (6 stages of 32 or 33 KB; two accumulators of 224 columns and the
-// scales fill tensor memory; two epilogue groups: with one, a prompt chunk's down
-// GEMM took 441 us instead of 345). The layer's single-CTA tiles run in
-// launch_mx4_experts.
+// Token tiles: 32, 64 or 128 rows on single CTAs (stages of 42 to 68 KB), 128 or
+// 224 rows on pairs (7 stages of 25 or 26 KB, 6 of 32 or 33 KB; two accumulators
+// of 224 columns and the scales fill tensor memory; two epilogue groups: with one, a
+// prompt chunk's down GEMM took 441 us instead of 345). The layer's single-CTA tiles
+// run in launch_mx4_experts.
 template <int MODE, bool F4>
 cudaError_t launch_mx4(const Mx4Args& a, const Mx4Tiling& t, int num_sms, size_t units, int splits,
                        cudaStream_t st) {
   if (t.pairs)
-    return launch_variant<MODE, F4, 2, kPairTile, 6, 1, 2, false>(a, num_sms, units, 1, st);
+    return t.rows == kPairTile
+               ? launch_variant<MODE, F4, 2, kPairTile, 6, 1, 2, false>(a, num_sms, units, 1, st)
+               : launch_variant<MODE, F4, 2, kSmallPairTile, 7, 1, 2, false>(a, num_sms, units, 1, st);
   if constexpr (MODE == kLinearMx4) {
     if (splits > 1)
       return t.rows == 32
                  ? launch_variant<MODE, F4, 1, 32, 4, 2, 1, true>(a, num_sms, units, splits, st)
                  : launch_variant<MODE, F4, 1, 64, 4, 2, 1, true>(a, num_sms, units, splits, st);
-    return t.rows == 32 ? launch_variant<MODE, F4, 1, 32, 4, 2, 1, false>(a, num_sms, units, 1, st)
-                        : launch_variant<MODE, F4, 1, 64, 4, 2, 1, false>(a, num_sms, units, 1, st);
+    return t.rows == 32   ? launch_variant<MODE, F4, 1, 32, 4, 2, 1, false>(a, num_sms, units, 1, st)
+           : t.rows == 64 ? launch_variant<MODE, F4, 1, 64, 4, 2, 1, false>(a, num_sms, units, 1, st)
+                          : launch_variant<MODE, F4, 1, 128, 3, 2, 1, false>(a, num_sms, units, 1, st);
   }
   return cudaErrorInvalidValue;
 }
@@ -1079,10 +1082,10 @@ bool set_tokens(Mx4Phase& a, int i, const TokenMaps& t, const Mx4Tiling& tl) {
   const uint64_t cols = (uint64_t)t.kt * (F4 ? 64 : 128);
   a.sB[i] = t.s;
   if (!tl.pairs) return make_tma_map(&a.tmB[i][0], t.q, MOE_DTYPE_E4M3, t.rows, cols, tl.rows);
-  using C = Mx4Cfg<kDownMx4, F4, 2, kPairTile, 6, 1, 2, false>;
   for (int b = 0; b < 5; ++b)
     if (!make_tma_map(&a.tmB[i][b], t.q, MOE_DTYPE_E4M3, t.rows, cols, pair_box(b))) return false;
-  return make_scale_tile_map(&a.tmSB[i], t.s, t.tiles * t.kt * C::RA, C::KT_STAGE * C::RA);
+  return make_scale_tile_map(&a.tmSB[i], t.s, t.tiles * t.kt * tl.row_atoms,
+                             (F4 ? 2 : 1) * tl.row_atoms);
 }
 
 template <bool F4>
@@ -1108,10 +1111,15 @@ bool set_weights(Mx4Phase& a, int i, const uint8_t* q, const uint8_t* s, uint64_
 //   10 of 512, 4096x1024  109/112/137  390/395/463  573/579/666  601/607/690  636/638/727
 //     Zipf                 74/75/96    126/123/154  229/209/238  328/284/298  513/419/399
 //   2 of 8, 4096x2048      44/56/53     44/44/57     62/53/64     85/63/71    143/99/96
-Mx4Tiling mx4_tiling(int64_t T, int tile) {
+Mx4Tiling mx4_tiling(int64_t T, int64_t k, int64_t E, int tile) {
   if (tile == MOE_TILE_AUTO)
     tile = T <= 64 ? MOE_TILE_DECODE : (T <= 512 ? MOE_TILE_MEDIUM : MOE_TILE_PREFILL);
-  if (tile == MOE_TILE_PREFILL) return {true, kPairTile, 32, 2};
+  // The smaller pair tile, with seven stages instead of six, while experts have few
+  // tokens on average (8 of 128, T = 1024, 64 an expert: 305 us, 328 us with 224 rows;
+  // T = 2048, 128 an expert: 396 us, 371 us; 10 of 512, Zipf, T = 1024: 376 us, 394 us).
+  if (tile == MOE_TILE_PREFILL)
+    return T * k <= 96 * E ? Mx4Tiling{true, kSmallPairTile, 32, 1}
+                           : Mx4Tiling{true, kPairTile, 32, 2};
   return {false, tile == MOE_TILE_MEDIUM ? 64 : 32, 16, 1};
 }
 
@@ -1173,7 +1181,7 @@ cudaError_t launch_grouped(const GemmProblem& p, const Mx4Weights& w, const Mx4T
                            cudaStream_t st) {
   Mx4Args a;
   memset(&a, 0, sizeof(a));
-  const Mx4Tiling tl = mx4_tiling(p.T, p.tile);
+  const Mx4Tiling tl = mx4_tiling(p.T, p.k, p.E, p.tile);
   if (!set_phase(a.ph[0], p, MODE == kGatedMx4, w, x, out, tl)) return cudaErrorInvalidValue;
   set_problem(a, p, offsets, status);
   return launch_mx4<MODE, false>(a, tl, p.num_sms, phase_units(p, a.ph[0], tl), 1, st);
@@ -1197,14 +1205,14 @@ cudaError_t launch_mx4_down_gemm(const GemmProblem& p, const Mx4Weights& w, cons
 // Both GEMMs of a batch on single-CTA tiles in one cooperative launch: its CTAs
 // wait for one another's h rows, so all of them have to be resident.
 int64_t mx4_done_counters(int64_t T, int64_t k, int64_t E, int tile) {
-  const Mx4Tiling tl = mx4_tiling(T, tile);
+  const Mx4Tiling tl = mx4_tiling(T, k, E, tile);
   return group_scale_tile(T * k, (int)E, tl.rows) + 1 + (T + tl.rows - 1) / tl.rows;
 }
 
 cudaError_t launch_mx4_experts(const GemmProblem& p, const Mx4Weights& w, const Mx4Tokens& x,
                                const int32_t* offsets, const Mx4Out& h, const Mx4Slots& y,
                                int* done, int* status, cudaStream_t st) {
-  const Mx4Tiling tl = mx4_tiling(p.T, p.tile);
+  const Mx4Tiling tl = mx4_tiling(p.T, p.k, p.E, p.tile);
   if (tl.pairs) return cudaErrorInvalidValue;
   Mx4Args a;
   memset(&a, 0, sizeof(a));
@@ -1225,15 +1233,24 @@ cudaError_t launch_mx4_experts(const GemmProblem& p, const Mx4Weights& w, const 
 Mx4LinearPlan mx4_linear_plan(int64_t T, int64_t N, int64_t K, int num_sms) {
   const int64_t kt = mxfp4_k_tiles(K);
   const int64_t blocks = (N + 127) / 128;
-  // Pairs when they fill at least half of the GPU (mxfp8, 16384 x 7168: T = 128,
-  // 16.8 us on pairs, 24.9 us on 64-row tiles; 4096 x 4096, T = 256 on 32 pairs,
-  // 12.0 us, 11.4 us).
+  // Above 128 tokens: pairs when they fill at least half of the GPU (16384 x 7168,
+  // T = 256: 27 us, 43 us on 64-row tiles; 4096 x 4096, T = 256 on 32 pairs: 12.0
+  // us, 11.4 us) or single CTAs do not run at once (8192 x 8192, T = 192 on 32
+  // pairs: 23.7 us, 26.9 us). Of the two pair tiles the smaller, which leaves room for
+  // a stage more, where it makes no more tiles (T = 256: 31.6 us, 33.9 us).
+  const bool wide = blocks * 2 > num_sms;  // two tiles of 64 rows do not run at once
   const int64_t pair_units = (blocks + 1) / 2 * ((T + kPairTile - 1) / kPairTile);
-  if (T > 64 && pair_units * 4 >= num_sms) return {{true, kPairTile, 32, 2}, 1};
-  // 64-row tiles stream the weights once for up to 64 tokens (16384 x 7168, T = 48:
-  // 15.5 us, 22.2 us as two tiles of 32); 32 rows leave room for deeper stages'
-  // worth of weights (T = 16: 14.7 us, 21.6 us with 64).
-  const int rows = T <= 32 ? 32 : 64;
+  if (T > 128 && (pair_units * 4 >= num_sms || blocks * ((T + 63) / 64) > num_sms))
+    return {(T + kPairTile - 1) / kPairTile == (T + kSmallPairTile - 1) / kSmallPairTile
+                ? Mx4Tiling{true, kSmallPairTile, 32, 1}
+                : Mx4Tiling{true, kPairTile, 32, 2},
+            1};
+  // A tile that holds all tokens streams the weights once (16384 x 7168, T = 48:
+  // 15.5 us, 22.2 us as two tiles of 32; T = 128: 20.7 us, 24.8 us as two of 64), a
+  // lower one has room for more weights in flight (T = 16: 14.7 us with 32 rows, 21.6
+  // us with 64), and two that run at once split the work (mxfp4, 8192 x 8192, T = 128:
+  // 12.4 us, 14.5 us as one).
+  const int rows = T <= 32 ? 32 : (wide && T > 64 && T <= 128 ? 128 : 64);
   const int64_t units = blocks * ((T + rows - 1) / rows);
   // As many CTAs per tile as still fit the GPU at once and leave each at least
   // 1024 of K (two to four stages): 4096 x 4096, T = 1, 6.7 us in clusters of

@@ -221,7 +221,7 @@ struct Mx4Tiling {
   bool pairs;  // CTA pairs (cta_group::2)
   int rows, unit, row_atoms;
 };
-Mx4Tiling mx4_tiling(int64_t T, int tile);
+Mx4Tiling mx4_tiling(int64_t T, int64_t k, int64_t E, int tile);
 // The token operand of the MXFP4 products: x [T][K] bf16 (row stride ld) ->
 // codes and, per token tile, its scale tiles. Routed: rows at their slots'
 // positions (checked: MOE_ERR_DEVICE_CHECK), and in token order into shared_q

@@ -83,13 +83,13 @@ int act_dtype(int dtype) {
 // Bytes of the scale tiles of an MXFP4 layer's routed (by expert) or shared (in
 // token order) token rows of `cols` elements.
 size_t mx4_routed_scale_bytes(const moe_problem& p, int64_t cols) {
-  const Mx4Tiling t = mx4_tiling(p.T, p.tile);
+  const Mx4Tiling t = mx4_tiling(p.T, p.k, p.E, p.tile);
   return (size_t)(group_scale_tile(p.T * p.k, (int)p.E, t.rows) + 1) *
          (size_t)mxfp4_k_tiles(cols) * (size_t)t.row_atoms * 512;
 }
-size_t mx4_token_scale_bytes(int64_t T, int tile, int64_t cols) {
-  const Mx4Tiling t = mx4_tiling(T, tile);
-  return (size_t)((T + t.rows - 1) / t.rows) * (size_t)mxfp4_k_tiles(cols) *
+size_t mx4_token_scale_bytes(const moe_problem& p, int64_t cols) {
+  const Mx4Tiling t = mx4_tiling(p.T, p.k, p.E, p.tile);
+  return (size_t)((p.T + t.rows - 1) / t.rows) * (size_t)mxfp4_k_tiles(cols) *
          (size_t)t.row_atoms * 512;
 }
 
@@ -143,10 +143,10 @@ Layout layout_of(const moe_problem& p) {
     L.hss = p.I_shared > 0 ? take(T * (size_t)moe_mx_scale_cols(p.I_shared)) : 0;
   } else if (m4) {
     L.xq = p.I_shared > 0 ? take(T * (size_t)p.H) : 0;
-    L.xs = p.I_shared > 0 ? take(mx4_token_scale_bytes(p.T, p.tile, p.H)) : 0;
+    L.xs = p.I_shared > 0 ? take(mx4_token_scale_bytes(p, p.H)) : 0;
     L.xgs = take(mx4_routed_scale_bytes(p, p.H));
     L.hsc = take(mx4_routed_scale_bytes(p, p.I));
-    L.hss = p.I_shared > 0 ? take(mx4_token_scale_bytes(p.T, p.tile, p.I_shared)) : 0;
+    L.hss = p.I_shared > 0 ? take(mx4_token_scale_bytes(p, p.I_shared)) : 0;
   } else {
     L.xs = L.xgs = L.hsc = L.hss = 0;
   }
@@ -159,7 +159,7 @@ Layout layout_of(const moe_problem& p) {
   L.shs = f8 && p.I_shared > 0 ? take(T * 4) : 0;
   L.Y = take(T * KP * (size_t)p.H * (m4 ? 2 : 4));
   L.ys = m4 ? take(T * KP * (size_t)(p.H / 32)) : 0;
-  L.done = m4 && !mx4_tiling(p.T, p.tile).pairs
+  L.done = m4 && !mx4_tiling(p.T, p.k, p.E, p.tile).pairs
                ? take((size_t)mx4_done_counters(p.T, p.k, p.E, p.tile) * 4)
                : 0;
   // Single-launch decode kernel: per-group counts of finished gate/up units.
@@ -907,7 +907,7 @@ moe_status moe_forward_mxfp4(const moe_problem* pb, const void* x, const void* W
     a.K = g.H;
     a.k = g.k;
     a.E = g.E;
-    a.tiling = mx4_tiling(g.T, g.tile);
+    a.tiling = mx4_tiling(g.T, g.k, g.E, g.tile);
     a.q = at<uint8_t>(workspace, L.xg);
     a.s = at<uint8_t>(workspace, L.xgs);
     a.shared_q = xq;

@@ -364,3 +364,12 @@ def test_example_block():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, y)
+
+
+@pytest.mark.parametrize("act", ["mxfp8", "mxfp4"])
+@pytest.mark.parametrize("T,N,K", [(65, 9900, 200), (128, 10240, 384), (129, 9900, 330),
+                                   (250, 4900, 1000), (256, 20000, 130), (449, 5000, 260)])
+def test_linear_tilings_of_wide_products(act, T, N, K):
+    """One tile of 128 rows, and pairs on tiles of 128 and of 224."""
+    x, W = _linear_case(T, N, K, seed=T)
+    _check_linear(x, W, act)
