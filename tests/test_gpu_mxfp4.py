@@ -373,3 +373,12 @@ def test_linear_tilings_of_wide_products(act, T, N, K):
     """One tile of 128 rows, and pairs on tiles of 128 and of 224."""
     x, W = _linear_case(T, N, K, seed=T)
     _check_linear(x, W, act)
+
+
+@pytest.mark.parametrize("T", [20, 100, 600])
+def test_layer_most_experts(T):
+    """The largest number of experts: the schedules take the most shared memory."""
+    cfg = MoEConfig("most", T=T, H=128, E=1024, k=4, I=128)
+    d, lay = _layer(cfg, seed=T)
+    _close(lay(d["x"], out_f32=True), _reference(cfg, d)[0])
+    assert m.get_device_status(lay.workspace(T)) == m.MOE_OK
